@@ -395,6 +395,111 @@ mla_status mla_combine_out_proj(const mla_config* cfg, const void* decode_ws, si
                                 void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Ragged steps (not on the pages: what a serving loop with requests of
+ * different lengths needs around the five steps).  Batch of `batch` sequences,
+ * sequence b with its own number of new tokens (none, one, or a prompt's
+ * chunk); all new tokens lie one behind the other in token arrays of n_tok
+ * rows, sequence b's in rows [cu_q[b], cu_q[b + 1]).  Rows from cu_q[batch] on
+ * are padding (a captured graph's arrays are sized for its largest step).
+ *
+ * mla_batch_tables - the step's bookkeeping on the device, from the requests'
+ * lengths.  Request b has cached_lens[b] rows in the cache and new_lens[b] new
+ * tokens; the pages it lacks for them are taken from the free list, in the
+ * order of the requests, and entered into its block table row.
+ *   cached_lens, new_lens  int32 [batch]
+ *   free_blocks  int32 [n_free], *free_head the first entry not yet handed out
+ *   block_table  int32 [batch, max_blocks_per_seq], in and out: the entries of
+ *                the pages that hold cached rows are read, those of new pages
+ *                written, no other is touched
+ *   cu_q      int32 [batch + 1]  first token row of each request, and their sum (out)
+ *   seq_lens  int32 [batch]      cached_lens + new_lens (out; may be cached_lens itself)
+ *   seq_idx   int32 [n_tok]      request of each token, -1 in padding rows (out)
+ *   pos       int32 [n_tok]      position of each token, 0 in padding rows (out)
+ *   slots     int64 [n_tok]      block id * block_size + row, where the token's
+ *                                cache row goes; -1 in padding rows (out)
+ *   free_head_out  int32 [1]     *free_head plus the pages taken (may be free_head itself)
+ *   num_blocks: blocks of the pool, to check block ids against.
+ * Any other overlap of outputs with inputs or with one another is not allowed.
+ * batch <= 16384, max_blocks_per_seq * block_size < 2^31 (MLA_ERR_UNSUPPORTED).
+ * Device errors (MLA_ERR_BOUNDS):
+ *   - a negative length, or more rows than a table row holds: that request
+ *     gets no tokens and seq_lens 0;
+ *   - requests that do not fit into the n_tok rows or the free list: the first
+ *     of them and all behind it get no tokens and no pages in this step
+ *     (seq_lens stays cached_lens, so the caller sees which);
+ *   - a block id outside the pool: slot -1 for its tokens.
+ *
+ * mla_cache_append_slots - mla_cache_append with the tokens' slots given
+ * instead of (sequence, position): row t goes to slot slots[t]; a slot of -1
+ * stores nothing (padding).  pos is the rotation's position.  Any other slot
+ * outside the pool -> MLA_ERR_BOUNDS, row not written.  Workspace as
+ * mla_cache_append.
+ * ------------------------------------------------------------------------- */
+mla_status mla_batch_tables(const mla_config* cfg, int32_t batch, const int32_t* cached_lens,
+                            const int32_t* new_lens, const int32_t* free_blocks, int32_t n_free,
+                            const int32_t* free_head, int32_t num_blocks, int32_t* block_table,
+                            int32_t max_blocks_per_seq, int32_t n_tok, int32_t* cu_q, int32_t* seq_lens,
+                            int32_t* seq_idx, int32_t* pos, int64_t* slots, int32_t* free_head_out,
+                            void* stream);
+mla_status mla_cache_append_slots(const mla_config* cfg, const void* x, int32_t n_tok, const void* W_DKV,
+                                  const void* W_KR, const int32_t* pos, const int64_t* slots,
+                                  const mla_cache* cache, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of a ragged batch's new tokens over the paged latent cache, in
+ * latent space as mla_decode, merged and rounded in the same call.  Sequence b
+ * has n_b = cu_q[b + 1] - cu_q[b] new tokens, already appended; token j of them
+ * (row t = cu_q[b] + j) stands at position p = seq_lens[b] - n_b + j and, per
+ * head h,
+ *   s_u = (q_lat[t,h] . c_u + q_rope[t,h] . kR_u) * scale     for its visible rows u
+ *   lse[t,h]   = log2 sum_u exp(s_u)
+ *   o_lat[t,h] = sum_u softmax(s)_u c_u.
+ * mla_chunk_attention: the rows u <= p.
+ * mla_window_attention: the rows u <= p with u > p - window or u < n_sinks (a
+ *   sliding window, its own row included, and the first n_sinks rows, which
+ *   stay visible).  Pages that no token sees are not read, so they may have
+ *   been given to other sequences; their table entries are not looked at.
+ * Rows that are not visible never enter the arithmetic, whatever they hold.
+ *   q        MLA_BF16 with a bf16 cache: packed rows [n_tok, H, d_c + d_r] bf16 of
+ *            mla_absorb_q_packed (twice that in split-query mode), q_rope NULL.
+ *            MLA_F32, or an FP8 cache: q_lat float32 [n_tok, H, d_c] and
+ *            q_rope float32 [n_tok, H, d_r] of mla_absorb_q.
+ *   cu_q     int32 [batch + 1], ascending from 0, last entry <= n_tok
+ *   seq_lens int32 [batch], new rows included; n_b <= seq_lens[b] <=
+ *            max_blocks_per_seq * block_size, or 0: an empty sequence, whose
+ *            tokens get o_lat 0 and lse -inf.  Sequences without new tokens are
+ *            passed over.
+ *   o_lat    [n_tok, H, d_c] storage dtype (out);  lse float32 [n_tok, H] (out) or NULL
+ *            Rows from cu_q[batch] on are left as they are.
+ *   max_workers: upper bound on parallel workers (0 = the device's).
+ *   workspace >= mla_chunk_workspace_size(cfg, n_tok, max_workers); it does
+ *            not grow with the lengths.
+ * 128 heads, d_c 512, d_r 64, pages of 64 and a bf16 cache run on the tensor
+ * cores; every other shape on CUDA cores (d_c + d_r <= 1024, any block_size).
+ * For a large FP8 cache expand the pages first (mla_cache_dequant_fp8).
+ * batch <= 8192 (MLA_ERR_UNSUPPORTED).  MLA_ERR_INVALID_ARG for window <= 0 or
+ * n_sinks < 0, pointers off their type's alignment (16 bytes on the tensor-core
+ * path).  Device errors (MLA_ERR_BOUNDS): entries of cu_q out of order (that
+ * sequence is passed over), a length that does not hold its tokens (their
+ * o_lat is 0), a block id outside the pool (that page is not visible).
+ *
+ * mla_out_proj_stored - mla_out_proj for an o_lat in the storage dtype.
+ * Workspace as mla_out_proj.
+ * ------------------------------------------------------------------------- */
+size_t mla_chunk_workspace_size(const mla_config* cfg, int32_t n_tok, int32_t max_workers);
+mla_status mla_chunk_attention(const mla_config* cfg, const void* q, const void* q_rope, int32_t n_tok,
+                               const int32_t* cu_q, int32_t batch, const mla_cache* cache,
+                               const int32_t* seq_lens, int32_t max_workers, void* o_lat, float* lse,
+                               void* workspace, size_t ws_bytes, void* stream);
+mla_status mla_window_attention(const mla_config* cfg, const void* q, const void* q_rope, int32_t n_tok,
+                                const int32_t* cu_q, int32_t batch, const mla_cache* cache,
+                                const int32_t* seq_lens, int32_t window, int32_t n_sinks,
+                                int32_t max_workers, void* o_lat, float* lse, void* workspace,
+                                size_t ws_bytes, void* stream);
+mla_status mla_out_proj_stored(const mla_config* cfg, const void* o_lat, int32_t n_tok, const void* W_UV,
+                               const void* W_O, void* y, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Errors and introspection
  * ------------------------------------------------------------------------- */
 /* Synchronises `stream`, returns the first device-side error recorded on the

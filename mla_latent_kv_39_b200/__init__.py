@@ -14,9 +14,13 @@ from .abi import (  # noqa: F401
     mla_absorb_q,
     mla_absorb_q_packed,
     mla_absorb_q_workspace_size,
+    mla_batch_tables,
     mla_cache_append,
     mla_cache_append_workspace_size,
     mla_cache_append_noalloc,
+    mla_cache_append_slots,
+    mla_chunk_attention,
+    mla_chunk_workspace_size,
     mla_combine,
     mla_combine_lse,
     mla_cache_dequant_fp8,
@@ -33,8 +37,10 @@ from .abi import (  # noqa: F401
     mla_kernel_launches,
     mla_merge_shards,
     mla_out_proj,
+    mla_out_proj_stored,
     mla_out_proj_workspace_size,
     mla_query_packed_bytes,
+    mla_window_attention,
 )
 from .layer import DecodeLayer  # noqa: F401
 from .shard import ShardPlan, decode_shard, decode_sharded, gather_partials, shard_plan  # noqa: F401

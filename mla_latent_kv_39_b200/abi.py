@@ -80,6 +80,14 @@ SIGNATURES = {
     "mla_combine_out_proj": (_i32, [_P_CFG, _vp, _sz, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mla_out_proj_workspace_size": (_sz, [_P_CFG, _i32]),
     "mla_out_proj": (_i32, [_P_CFG, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mla_batch_tables": (_i32, [_P_CFG, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                                _vp, _vp]),
+    "mla_cache_append_slots": (_i32, [_P_CFG, _vp, _i32, _vp, _vp, _vp, _vp, _P_CACHE, _vp, _sz, _vp]),
+    "mla_chunk_workspace_size": (_sz, [_P_CFG, _i32, _i32]),
+    "mla_chunk_attention": (_i32, [_P_CFG, _vp, _vp, _i32, _vp, _i32, _P_CACHE, _vp, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "mla_window_attention": (_i32, [_P_CFG, _vp, _vp, _i32, _vp, _i32, _P_CACHE, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
+                                    _sz, _vp]),
+    "mla_out_proj_stored": (_i32, [_P_CFG, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mla_get_device_error": (_i32, [_vp, ctypes.POINTER(_i32)]),
     "mla_check_wait_timeout": (_i32, [ctypes.c_int64, _vp]),
 }
@@ -427,6 +435,130 @@ def mla_out_proj(cfg: Config, o_lat, W_UV, W_O, y, workspace, stream=None):
     _need(workspace, "workspace", torch.uint8)
     _check(lib().mla_out_proj(ctypes.byref(cfg.c()), _ptr(o_lat), n, _ptr(W_UV), _ptr(W_O), _ptr(y),
                               _ptr(workspace), workspace.numel(), _stream(stream)), "mla_out_proj")
+
+
+# --------------------------------------------------------------- ragged steps
+
+def _need_here(**tensors):
+    """Every given tensor is on the current device (the library launches there)."""
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{name} must be on the current device cuda:{here}, got {t.device}")
+
+
+def mla_batch_tables(cfg: Config, cached_lens, new_lens, free_blocks, free_head, num_blocks: int, block_table, cu_q,
+                     seq_lens, seq_idx, pos, slots, free_head_out=None, stream=None):
+    """Block tables, prefix, positions and slots of a ragged step (``include/mla.h``).
+
+    ``block_table`` is extended in place with pages from ``free_blocks``; the cursor ``free_head`` moves on in
+    ``free_head_out`` (default: in place).  ``seq_lens`` may be ``cached_lens``.  The token arrays ``seq_idx``,
+    ``pos`` and ``slots`` are padded with -1, 0 and -1 behind the last token."""
+    batch, n_tok = cached_lens.shape[0], pos.shape[0]
+    i32 = torch.int32
+    free_head_out = free_head if free_head_out is None else free_head_out
+    _need(cached_lens, "cached_lens", i32, shape=(batch,))
+    _need(new_lens, "new_lens", i32, shape=(batch,))
+    _need(free_blocks, "free_blocks", i32, ndim=1)
+    _need(free_head, "free_head", i32, shape=(1,))
+    _need(free_head_out, "free_head_out", i32, shape=(1,))
+    _need(block_table, "block_table", i32, ndim=2)
+    if block_table.shape[0] != batch:
+        raise ValueError(f"block_table must have {batch} rows, got {tuple(block_table.shape)}")
+    _need(cu_q, "cu_q", i32, shape=(batch + 1,))
+    _need(seq_lens, "seq_lens", i32, shape=(batch,))
+    _need(seq_idx, "seq_idx", i32, shape=(n_tok,))
+    _need(pos, "pos", i32, shape=(n_tok,))
+    _need(slots, "slots", torch.int64, shape=(n_tok,))
+    _need_here(cached_lens=cached_lens, new_lens=new_lens, free_blocks=free_blocks, block_table=block_table, pos=pos)
+    _check(lib().mla_batch_tables(ctypes.byref(cfg.c()), batch, _ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks),
+                                  free_blocks.shape[0], _ptr(free_head), num_blocks, _ptr(block_table),
+                                  block_table.shape[1], n_tok, _ptr(cu_q), _ptr(seq_lens), _ptr(seq_idx), _ptr(pos),
+                                  _ptr(slots), _ptr(free_head_out), _stream(stream)), "mla_batch_tables")
+
+
+def mla_cache_append_slots(cfg: Config, x, W_DKV, W_KR, pos, slots, cache: Cache, workspace, stream=None):
+    """``mla_cache_append`` with the tokens' slots given; a slot of -1 (padding) stores nothing."""
+    dt = cfg.torch_dtype
+    n = x.shape[0]
+    _need(x, "x", dt, shape=(n, cfg.hidden))
+    _need(W_DKV, "W_DKV", dt, shape=(cfg.hidden, cfg.d_c))
+    _need(W_KR, "W_KR", dt, shape=(cfg.hidden, cfg.d_r))
+    _need(pos, "pos", torch.int32, shape=(n,))
+    _need(slots, "slots", torch.int64, shape=(n,))
+    _need(workspace, "workspace", torch.uint8)
+    if cache.pool.dtype != cfg.cache_torch_dtype or cache.pool.shape[1:] != (cfg.block_size, cfg.d_c + cfg.d_r):
+        raise ValueError("cache pool dtype/shape does not match the config")
+    _need_here(x=x, slots=slots, pool=cache.pool, workspace=workspace)
+    _check(lib().mla_cache_append_slots(ctypes.byref(cfg.c()), _ptr(x), n, _ptr(W_DKV), _ptr(W_KR), _ptr(pos),
+                                        _ptr(slots), ctypes.byref(cache.c), _ptr(workspace), workspace.numel(),
+                                        _stream(stream)), "mla_cache_append_slots")
+
+
+def mla_chunk_workspace_size(cfg: Config, n_tok: int, max_workers: int = 0) -> int:
+    return int(lib().mla_chunk_workspace_size(ctypes.byref(cfg.c()), n_tok, max_workers))
+
+
+def _chunk_args(cfg: Config, q, cu_q, cache: Cache, seq_lens, o_lat, workspace, lse):
+    """Checked arguments of the two ragged attentions: (n_tok, batch, q, q_rope)."""
+    n, H = o_lat.shape[0], cfg.n_heads
+    batch = seq_lens.shape[0]
+    if isinstance(q, torch.Tensor):
+        if cfg.dtype != "bf16" or cfg.fp8_cache:
+            raise TypeError("q must be the pair (q_lat, q_rope) for fp32 storage or an FP8 cache")
+        _need(q, "q", torch.bfloat16, shape=((2 if cfg.split_query else 1) * n, H, cfg.d_c + cfg.d_r))
+        q_lat, q_rope = q, None
+    else:
+        if cfg.dtype == "bf16" and not cfg.fp8_cache:
+            raise TypeError("q must be the packed bf16 rows for a bf16 cache")
+        q_lat, q_rope = q
+        _need(q_lat, "q_lat", torch.float32, shape=(n, H, cfg.d_c))
+        _need(q_rope, "q_rope", torch.float32, shape=(n, H, cfg.d_r))
+    _need(cu_q, "cu_q", torch.int32, shape=(batch + 1,))
+    _need(seq_lens, "seq_lens", torch.int32, shape=(batch,))
+    _need(o_lat, "o_lat", cfg.torch_dtype, shape=(n, H, cfg.d_c))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, shape=(n, H))
+    _need(workspace, "workspace", torch.uint8)
+    if cache.pool.dtype != cfg.cache_torch_dtype or cache.pool.shape[1:] != (cfg.block_size, cfg.d_c + cfg.d_r):
+        raise ValueError("cache pool dtype/shape does not match the config")
+    _need_here(q=q_lat, cu_q=cu_q, seq_lens=seq_lens, pool=cache.pool, o_lat=o_lat, lse=lse, workspace=workspace)
+    return n, batch, q_lat, q_rope
+
+
+def mla_chunk_attention(cfg: Config, q, cu_q, cache: Cache, seq_lens, o_lat, workspace, lse=None, max_workers: int = 0,
+                        stream=None):
+    """Ragged causal attention of new tokens over the paged cache (``include/mla.h``).  ``q``: the packed bf16 rows,
+    or for fp32 storage and an FP8 cache the pair ``(q_lat, q_rope)``.  Rows of ``o_lat`` and ``lse`` from
+    ``cu_q[-1]`` on keep what they hold."""
+    n, batch, q_lat, q_rope = _chunk_args(cfg, q, cu_q, cache, seq_lens, o_lat, workspace, lse)
+    _check(lib().mla_chunk_attention(ctypes.byref(cfg.c()), _ptr(q_lat), _ptr(q_rope), n, _ptr(cu_q), batch,
+                                     ctypes.byref(cache.c), _ptr(seq_lens), max_workers, _ptr(o_lat), _ptr(lse),
+                                     _ptr(workspace), workspace.numel(), _stream(stream)), "mla_chunk_attention")
+
+
+def mla_window_attention(cfg: Config, q, cu_q, cache: Cache, seq_lens, window: int, n_sinks: int, o_lat, workspace,
+                         lse=None, max_workers: int = 0, stream=None):
+    """``mla_chunk_attention`` over a sliding window of ``window`` rows and the first ``n_sinks`` rows."""
+    n, batch, q_lat, q_rope = _chunk_args(cfg, q, cu_q, cache, seq_lens, o_lat, workspace, lse)
+    _check(lib().mla_window_attention(ctypes.byref(cfg.c()), _ptr(q_lat), _ptr(q_rope), n, _ptr(cu_q), batch,
+                                      ctypes.byref(cache.c), _ptr(seq_lens), window, n_sinks, max_workers, _ptr(o_lat),
+                                      _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)),
+           "mla_window_attention")
+
+
+def mla_out_proj_stored(cfg: Config, o_lat, W_UV, W_O, y, workspace, stream=None):
+    """``mla_out_proj`` for an ``o_lat`` in the storage dtype."""
+    dt = cfg.torch_dtype
+    n = o_lat.shape[0]
+    H = cfg.n_heads
+    _need(o_lat, "o_lat", dt, shape=(n, H, cfg.d_c))
+    _need(W_UV, "W_UV", dt, shape=(cfg.d_c, H * cfg.v_head))
+    _need(W_O, "W_O", dt, shape=(H * cfg.v_head, cfg.hidden))
+    _need(y, "y", dt, shape=(n, cfg.hidden))
+    _need(workspace, "workspace", torch.uint8)
+    _check(lib().mla_out_proj_stored(ctypes.byref(cfg.c()), _ptr(o_lat), n, _ptr(W_UV), _ptr(W_O), _ptr(y),
+                                     _ptr(workspace), workspace.numel(), _stream(stream)), "mla_out_proj_stored")
 
 
 def mla_get_device_error(stream=None):

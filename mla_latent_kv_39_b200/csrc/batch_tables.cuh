@@ -1,0 +1,223 @@
+// Block tables, positions and slot maps of a ragged step, from the requests'
+// lengths.
+//
+// Request b holds cached[b] rows in its pages and brings new_[b] tokens.  Its
+// table has have = ceil(cached / bs) pages and needs ceil((cached + new) / bs):
+// the missing ones are taken from the free list, in the order of the requests.
+// With the two prefix sums over the requests
+//   cu[b]    = sum of new over the requests before b
+//   first[b] = sum of missing pages over the requests before b
+// every output is an independent gather: page k >= have of request b is
+// free[head + first[b] + k - have]; token t of request b stands at position
+// cached + t - cu[b], in slot page * bs + position mod bs.
+//
+// Requests whose tokens or pages do not fit any more (and all behind them) get
+// no tokens and no pages; both prefix sums only grow, so "fits" is a prefix of
+// the requests.
+//
+// What bounds it is latency: 8 bytes read a request, 16 bytes written a token.
+// One cluster of up to 8 CTAs, each of which makes both prefix sums for itself
+// (a scan of at most 16,384 values costs less than handing them round) and
+// then fills its share of the tokens.  Inputs that an output may replace (the
+// lengths by seq_lens, the cursor by its new value) are read by all CTAs before
+// the cluster's barrier and written behind it; one launch and no workspace.
+#pragma once
+
+#include "decode_pair.cuh"
+
+namespace mla {
+namespace tables {
+
+constexpr int kMaxBatch = 16384;  // requests of a call: two prefix sums in shared memory
+constexpr int kThreads = 1024;
+
+struct Args {
+  int batch, bs, n_free, num_blocks, max_blocks, n_tok;
+  const int32_t* cached;
+  const int32_t* new_;
+  const int32_t* free_blocks;
+  const int32_t* free_head;
+  int32_t* block_table;
+  int32_t* cu_q;
+  int32_t* seq_lens;
+  int32_t* seq_idx;
+  int32_t* pos;
+  long long* slots;
+  int32_t* head_out;
+};
+
+__device__ __forceinline__ int pages_of(int rows, int bs) { return rows / bs + (rows % bs != 0); }
+
+// Inclusive sums over the block of two values per thread (64 bits: a sum of
+// lengths that do not fit may pass 31).
+__device__ __forceinline__ void scan2(long long& x, long long& y, long long (*tot)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += a;
+      y += b;
+    }
+  }
+  if (lane == 31) {
+    tot[warp][0] = x;
+    tot[warp][1] = y;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long a = tot[lane][0], b = tot[lane][1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long c = __shfl_up_sync(0xffffffffu, a, o), d = __shfl_up_sync(0xffffffffu, b, o);
+      if (lane >= o) {
+        a += c;
+        b += d;
+      }
+    }
+    tot[lane][0] = a;
+    tot[lane][1] = b;
+  }
+  __syncthreads();
+  if (warp > 0) {
+    x += tot[warp - 1][0];
+    y += tot[warp - 1][1];
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
+  extern __shared__ int sm[];
+  int* cu = sm;                      // [batch + 1]
+  int* first = sm + a.batch + 1;     // [batch + 1]
+  int* len = sm + 2 * (a.batch + 1); // [batch] cached rows
+  __shared__ long long tot[32][2];
+  __shared__ int served;
+  const int tid = threadIdx.x, rank = (int)sm100::cluster_ctarank(), ctas = gridDim.x;
+  pdl_wait();
+  pdl_trigger();
+
+  int head = *a.free_head;
+  const bool bad_head = head < 0 || head > a.n_free;
+  if (bad_head) head = a.n_free;  // nothing to hand out
+  const int avail = a.n_free - head;
+  const int per = pages_of(a.batch, kThreads);
+  const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+  long long n = 0, pages = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int c = a.cached[b], w = a.new_[b];
+    const bool bad = c < 0 || w < 0 || (long long)c + w > (long long)a.max_blocks * a.bs;
+    if (bad && rank == 0) report(MLA_ERR_BOUNDS, 30, b, c < 0 ? c : w);
+    len[b] = bad ? -1 : c;
+    // until the scan: this request's own counts
+    cu[b + 1] = bad ? 0 : w;
+    first[b + 1] = bad ? 0 : pages_of(c + w, a.bs) - pages_of(c, a.bs);
+    n += cu[b + 1];
+    pages += first[b + 1];
+  }
+  if (tid == 0) {
+    served = a.batch;
+    cu[0] = first[0] = 0;
+    if (bad_head && rank == 0) report(MLA_ERR_BOUNDS, 33, *a.free_head, a.n_free);
+  }
+  const long long own_n = n, own_p = pages;
+  scan2(n, pages, tot);
+  n -= own_n;
+  pages -= own_p;
+  int miss = a.batch;  // the first request of this thread's that does not fit
+  for (int b = b0; b < b1; ++b) {
+    n += cu[b + 1];
+    pages += first[b + 1];
+    if (n > a.n_tok || pages > avail) {
+      miss = b;
+      break;
+    }
+    cu[b + 1] = (int)n;
+    first[b + 1] = (int)pages;
+  }
+  if (miss < a.batch) atomicMin(&served, miss);
+  __syncthreads();
+  const int S = served;
+  if (S < a.batch) {
+    // the requests from S on: nothing new (their entries may hold raw counts)
+    for (int b = S + tid; b < a.batch; b += kThreads) {
+      cu[b + 1] = cu[S];
+      first[b + 1] = first[S];
+    }
+    if (tid == 0 && rank == 0) report(MLA_ERR_BOUNDS, 31, S, a.batch);
+    __syncthreads();
+  }
+  const int total = cu[a.batch];
+  sm100::cluster_sync();  // every CTA has read the lengths and the cursor
+
+  if (rank == 0) {
+    for (int b = tid; b <= a.batch; b += kThreads) {
+      a.cu_q[b] = cu[b];
+      if (b < a.batch) a.seq_lens[b] = len[b] < 0 ? 0 : len[b] + (cu[b + 1] - cu[b]);
+    }
+    if (tid == 0) *a.head_out = head + first[a.batch];
+  }
+  // new table entries: one per page taken
+  const int step = ctas * kThreads, me = rank * kThreads + tid;
+  for (int i = me; i < first[a.batch]; i += step) {
+    int lo = 0, hi = a.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    const int id = a.free_blocks[head + i];
+    a.block_table[(long long)lo * a.max_blocks + pages_of(len[lo], a.bs) + i - first[lo]] = id;
+    if (id < 0 || id >= a.num_blocks) report(MLA_ERR_BOUNDS, 32, lo, id);
+  }
+  // tokens
+  for (int t = me; t < a.n_tok; t += step) {
+    int b = -1, p = 0;
+    long long slot = -1;
+    if (t < total) {
+      int lo = 0, hi = a.batch - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+      p = len[b] + t - cu[b];
+      const int page = p / a.bs, have = pages_of(len[b], a.bs);
+      const int id = page < have ? a.block_table[(long long)b * a.max_blocks + page]
+                                 : a.free_blocks[head + first[b] + page - have];
+      if (id < 0 || id >= a.num_blocks) report(MLA_ERR_BOUNDS, 32, b, id);
+      else slot = (long long)id * a.bs + p % a.bs;
+    }
+    a.seq_idx[t] = b;
+    a.pos[t] = p;
+    a.slots[t] = slot;
+  }
+}
+
+// CTAs of the cluster: one fills 4,096 tokens in four rounds of its threads;
+// beyond that more of them share the tokens.
+inline int ctas_for(int n_tok) { return n_tok <= 4 * kThreads ? 1 : 8; }
+
+inline mla_status launch(const Args& a, cudaStream_t s) {
+  const size_t smem = sizeof(int) * (3 * (size_t)a.batch + 2);
+  static std::atomic<uint64_t> attr{0};
+  if (smem > 46 * 1024 &&
+      pairdec::set_smem_once((const void*)batch_tables_kernel, sizeof(int) * (3 * (size_t)kMaxBatch + 2), attr) != MLA_OK)
+    return MLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas_for(a.n_tok));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cfg.gridDim.x;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, batch_tables_kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace tables
+}  // namespace mla

@@ -1,0 +1,782 @@
+// Attention of a ragged batch's new tokens over the paged latent cache on pairs
+// of SMs (tcgen05 .cta_group::2), bf16, 128 heads, 512 + 64 wide rows.
+//
+// For every token t and head h, over the token's visible rows u
+// (chunk_plan.cuh):
+//   s_u = scale (q_lat . c_u + q_rope . k_R,u),   o_lat = sum_u softmax(s)_u c_u
+// in one pass with the running maximum and sum.  In the absorbed form every
+// head reads the same 576-wide row, so a token is a 128-row MMA operand and a
+// page serves as keys and as values.
+//
+// A worker is a cluster of two CTAs; CTA r holds heads [64 r, 64 r + 64) of
+// one token at a time: their scores and their whole 512-wide output fill its
+// tensor memory.  A tile is four items (pages) of the token:
+//   scores: pair MMAs M = 128 heads, N = 256 tokens, over 9 slabs of 64
+//           values; CTA r supplies items 2 r and 2 r + 1;
+//   P V:    pair MMAs M = 128, N = 256 latent columns, over 16 tokens a step;
+//           of column block j CTA r supplies columns 256 j + 128 r + (0..127).
+// N = 256 is what keeps the tensor pipe at its rate: a pair MMA with 64 rows
+// per SM takes as long for 128 columns as for 256 (measured back to back:
+// 64.8 clocks either way).
+//
+// Every operand slab is loaded by TMA into one ring of 16 KiB slots in the
+// order in which the MMAs take them:
+//   K(0), K(1), V(0), K(2), V(1), ...   (9 slots for K, 2 per page for V),
+// and the MMAs are issued in that order by one warp: the scores of tile i + 1
+// run ahead of P V of tile i, into the other of two score buffers, so the
+// softmax of a tile has the time of two MMA phases.  Keys are read a second
+// time as values (an L2 hit): holding them from the scores to P V would take
+// two tiles of shared memory, and the ring streams faster than the MMAs need.
+// One warp issues a load and its barrier work in about 420 clocks (19 B per
+// clock and SM), four warps 77 B per clock, so four warps take the ring's
+// slots in turn.
+//
+// TMEM (512 columns): scores [0, 128) and [128, 256), output [256, 512).
+// A pair MMA of M = 128 leaves a CTA's 64 rows in 128 lanes x N / 2 columns:
+// lane l holds head 64 r + (l mod 64), lanes 0..63 the first half of the N
+// columns and lanes 64..127 the second.  So the softmax thread of lane l and
+// column half ch owns one item of the tile, q = 2 (l / 64) + ch.
+//
+// Warp roles (448 threads): warps 0..7 softmax and output, warp 8 issues the
+// MMAs (leader CTA), warps 9..12 load the ring, warp 13 the queries.
+//
+// Rows that are not visible never reach an MMA: a page's box is shifted so
+// that they fall outside the page and arrive as zeros, or, when the range is
+// cut on both sides (only a window shorter than a page does that), it is read
+// through a tensor map that ends at the range's last row.
+//
+// A worker's range of work may begin or end inside a token.  A token that one
+// worker holds whole is written to o_lat at once, rounded once to bf16; the
+// pieces of the others go to the workspace in fp32 with their log2-sum-exp
+// (at most two pieces a worker, so the workspace does not grow with the
+// tokens) and chunk_merge_kernel joins them.
+//
+// Every wait gives up after a time limit, records MLA_ERR_TIMEOUT and makes
+// the roles wind down.
+#pragma once
+
+#include "chunk_plan.cuh"
+#include "decode_pair.cuh"
+
+namespace mla {
+namespace chunk {
+
+using namespace sm100;
+
+constexpr int kH = 128, kHalfH = 64, kDc = 512, kDr = 64, kRow = kDc + kDr;
+constexpr int kSlabs = kRow / 64;
+constexpr int kSlab = 64 * 128;  // 64 rows x 64 bf16, 128-byte swizzle
+constexpr int kKvSlot = 2 * kSlab;
+constexpr int kTmemS = 0, kTmemO = 256, kTmemCols = 512;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp0 = 9, kLoadWarps = 4, kQueryWarp = 13;
+constexpr int kThreads = 32 * 14;
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint16_t kBoth = 3;
+constexpr int kMaxWorkers = 1024;
+static_assert((kLoadWarps & (kLoadWarps - 1)) == 0, "slots are dealt to the load warps by a mask");
+
+// Ring slots: a key slab of two pages (in split-query mode followed by the
+// low part of the query's slab), or 128 value columns of one page.
+template <bool kSplit>
+struct Geo {
+  static constexpr int kSlot = kSplit ? kKvSlot + kSlab : kKvSlot;
+  static constexpr int kSlots = kSplit ? 4 : 7;
+};
+
+template <bool kSplit>
+struct Smem {
+  using G = Geo<kSplit>;
+  uint8_t q[kSlabs][kSlab];                  // 64 heads x 576 values, K-major slabs; first member: 1024-byte aligned
+  uint8_t p[kTilePages][kSlab];              // P of the tile: per item 64 heads x 64 tokens
+  uint8_t ring[G::kSlots][G::kSlot];         // the prefix sums of the cut, then the ring
+  uint64_t full[G::kSlots], empty[G::kSlots];
+  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, fin, xbar[2], lbar;
+  float xm[2][2][128];                       // [tile parity][column half] maximum of each lane's columns
+  float xl[2][2][128];                       // [piece parity][column half] partial row sums of a finished piece
+  long long warp_sum[kThreads / 32];
+  Place from, to;                            // this worker's range
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <bool kSplit>
+constexpr size_t smem_bytes() {
+  return sizeof(Smem<kSplit>) + 1024;
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "over the 227 KiB per-block limit");
+static_assert(sizeof(long long) * (kMaxBatch + 1) <= 4 * (kKvSlot + kSlab) &&
+                  sizeof(long long) * (kMaxBatch + 1) <= 7 * kKvSlot,
+              "the prefix sums fit the ring");
+
+// Workspace: per worker its two pieces (0: the rest of a token begun by an
+// earlier worker, 1: the beginning of a token that a later one goes on with).
+struct Layout {
+  int workers;
+  long long off_piece, off_lse, off_o, total;
+};
+inline Layout layout(int workers) {
+  Layout L{};
+  L.workers = workers;
+  size_t o = 0;
+  L.off_piece = o; o = align_up(o + sizeof(int4) * (size_t)workers, 256);
+  L.off_lse = o;   o = align_up(o + sizeof(float) * 2 * (size_t)workers * kH, 256);
+  L.off_o = o;     o = align_up(o + sizeof(float) * 2 * (size_t)workers * kH * kDc, 256);
+  L.total = o;
+  return L;
+}
+
+struct Params {
+  Batch q;
+  const int32_t* block_table;
+  int max_blocks, num_blocks;
+  float scale_log2;
+  unsigned long long wait_ns;
+  int workers;
+  int4* piece;      // a worker's Shares
+  float* part_lse;
+  float* part_o;
+  bf16* o_lat;
+  float* lse;
+};
+
+// Tensor maps of the pool: map r - 1 ends at row r of every page.  Only windows
+// shorter than a page read through any but the last.
+struct PoolMaps {
+  CUtensorMap end[kPage];
+};
+struct PoolMap {
+  CUtensorMap end[1];
+};
+
+__device__ __forceinline__ uint32_t leader(const uint64_t* bar) { return mapa(smem_u32(bar), 0); }
+__device__ __forceinline__ uint64_t kmajor(const void* p) { return smem_desc(smem_u32(p), 16, 1024, kSwizzle128B); }
+__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Lane 0 polls, the outcome is the warp's.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int where, uint64_t wns, int lane) {
+  int ok = 1;
+  if (lane == 0) ok = mbar_wait(bar, parity, where, wns) ? 1 : 0;
+  return uni(ok) != 0;
+}
+
+template <bool kSplit>
+__device__ __forceinline__ void set_abort(Smem<kSplit>& sm) {
+  *(volatile int*)&sm.abort_flag = 1;
+}
+template <bool kSplit>
+__device__ __forceinline__ bool aborted(Smem<kSplit>& sm) {
+  return uni(*(volatile int*)&sm.abort_flag) != 0;
+}
+
+// ---------------------------------------------------------------- the cut
+// Costs of the sequences, summed up in shared memory by all threads; then the
+// two ends of this worker's range.
+template <bool kSplit>
+__device__ void find_range(Smem<kSplit>& sm, const Params& p, int worker) {
+  long long* C = reinterpret_cast<long long*>(sm.ring);
+  const Batch& q = p.q;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (q.batch + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, q.batch), b1 = min(b0 + per, q.batch);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Sequence s = sequence_of(q, b);
+    if (blockIdx.x == 0) report_sequence(q, b, s);
+    mine += cost_of_tokens(q.vis, s, s.n);
+    C[b + 1] = mine;
+  }
+  long long x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sm.warp_sum[warp] = x;
+  __syncthreads();
+  long long ahead = x - mine;
+  for (int w = 0; w < warp; ++w) ahead += sm.warp_sum[w];
+  for (int b = b0; b < b1; ++b) C[b + 1] += ahead;
+  if (tid == 0) C[0] = 0;
+  __syncthreads();
+  if (warp < 2 && lane == 0) {
+    const Place at = cut(q, C, worker + warp, p.workers);
+    if (warp == 0) sm.from = at; else sm.to = at;
+  }
+}
+
+// ---------------------------------------------------------------- TMA producers
+// The four items of a tile as the loads need them.
+struct TileLoad {
+  int n;                        // items
+  int phys[kTilePages], y[kTilePages], m[kTilePages];  // page, first row of the box, tensor map
+};
+
+template <typename Maps>
+__device__ __forceinline__ TileLoad tile_load(const Params& p, const Walk& w, int tile, int lane) {
+  TileLoad t;
+  const int k0 = w.at.k + tile * kTilePages;
+  t.n = min(kTilePages, w.k1 - k0);
+  // lanes 0..3 look up one item each
+  int phys = 0, y = 0, m = 0;
+  if (lane < t.n) {
+    const Item it = item_of(p.q.vis, w.position(), k0 + lane);
+    phys = p.block_table[(long long)w.at.b * p.max_blocks + it.page];
+    if (phys < 0 || phys >= p.num_blocks) phys = p.num_blocks;  // outside the pool: arrives as zeros (masked too)
+    if (it.b == kPage) {
+      y = it.a;
+      m = sizeof(Maps) / sizeof(CUtensorMap) - 1;
+    } else if (it.a == 0 || sizeof(Maps) == sizeof(CUtensorMap)) {
+      y = it.b - kPage;  // rows past the range fall behind the page's top, negative rows arrive as zeros
+      m = sizeof(Maps) / sizeof(CUtensorMap) - 1;
+    } else {
+      y = it.a;
+      m = it.b - 1;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kTilePages; ++i) {
+    t.phys[i] = __shfl_sync(0xffffffffu, phys, i);
+    t.y[i] = __shfl_sync(0xffffffffu, y, i);
+    t.m[i] = __shfl_sync(0xffffffffu, m, i);
+  }
+  return t;
+}
+
+template <bool kSplit, typename Maps>
+struct Loader {
+  using G = Geo<kSplit>;
+  Smem<kSplit>& sm;
+  const Maps& pool;
+  const CUtensorMap* qlo;
+  const Params& p;
+  const int me, rank, lane;
+  int sl = 0, use = 0, g = 0;  // ring slot, its use, running count
+
+  __device__ bool mine() const { return (g & (kLoadWarps - 1)) == me; }
+  __device__ void step() {
+    ++g;
+    if (++sl == G::kSlots) {
+      sl = 0;
+      ++use;
+    }
+  }
+  __device__ bool ready() {
+    return use == 0 || warp_wait(&sm.empty[sl], (use - 1) & 1, 40, p.wait_ns, lane);
+  }
+  // the 9 key slabs of a tile of token `tok`
+  __device__ bool keys(const TileLoad& t, int tok) {
+#pragma unroll 1
+    for (int e = 0; e < kSlabs; ++e, step()) {
+      if (!mine()) continue;
+      if (!ready()) return false;
+      if (lane == 0) {
+        const uint32_t bar = leader(&sm.full[sl]);
+        if (rank == 0) mbar_arrive_expect_tx(&sm.full[sl], t.n * kSlab + (kSplit ? 2 * kSlab : 0));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = 2 * rank + h;
+          const int phys = rank ? t.phys[2 + h] : t.phys[h], y = rank ? t.y[2 + h] : t.y[h], m = rank ? t.m[2 + h] : t.m[h];
+          if (i < t.n) tma_load_3d_pair(sm.ring[sl] + h * kSlab, &pool.end[m], 64 * e, y, phys, bar);
+        }
+        if (kSplit) tma_load_2d_pair(sm.ring[sl] + kKvSlot, qlo, 64 * e, tok * kH + kHalfH * rank, bar);
+      }
+      __syncwarp();
+    }
+    return true;
+  }
+  // the value columns of a tile: per item two blocks of 256 columns
+  __device__ bool values(const TileLoad& t) {
+#pragma unroll
+    for (int i = 0; i < kTilePages; ++i) {
+      if (i >= t.n) break;
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j, step()) {
+        if (!mine()) continue;
+        if (!ready()) return false;
+        if (lane == 0) {
+          const uint32_t bar = leader(&sm.full[sl]);
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[sl], 2 * kKvSlot);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d_pair(sm.ring[sl] + h * kSlab, &pool.end[t.m[i]], 256 * j + 128 * rank + 64 * h, t.y[i], t.phys[i],
+                             bar);
+        }
+        __syncwarp();
+      }
+    }
+    return true;
+  }
+};
+
+template <bool kSplit, typename Maps>
+__device__ void load_role(Smem<kSplit>& sm, const Maps& pool, const CUtensorMap* qlo, const Params& p, int me, int rank,
+                          int lane) {
+  Loader<kSplit, Maps> ld{sm, pool, qlo, p, me, rank, lane};
+  TileLoad prev;
+  prev.n = 0;
+  bool ok = true;
+  for (Walk w(p.q, sm.from, sm.to); ok && w.valid(); w.next()) {
+    const int nt = w.tiles(), tok = w.token();
+    for (int i = 0; ok && i < nt; ++i) {
+      const TileLoad t = tile_load<Maps>(p, w, i, lane);
+      ok = ld.keys(t, tok) && ld.values(prev) && !aborted(sm);
+      prev = t;
+    }
+  }
+  if (ok) ok = ld.values(prev);
+  if (!ok) set_abort(sm);
+}
+
+template <bool kSplit>
+__device__ void query_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, int rank, int lane) {
+  int n = 0;
+  for (Walk w(p.q, sm.from, sm.to); w.valid(); w.next()) {
+    if (w.tiles() == 0) continue;
+    if (n >= 1 && !warp_wait(&sm.q_empty, (n - 1) & 1, 41, p.wait_ns, lane)) {
+      set_abort(sm);
+      return;
+    }
+    if (lane == 0) {
+      if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kSlabs * kSlab);
+      for (int e = 0; e < kSlabs; ++e)
+        tma_load_2d_pair(sm.q[e], qmap, 64 * e, w.token() * kH + kHalfH * rank, leader(&sm.q_full));
+    }
+    __syncwarp();
+    ++n;
+  }
+}
+
+// ---------------------------------------------------------------- MMA issuer (leader CTA)
+template <bool kSplit>
+struct Issuer {
+  using G = Geo<kSplit>;
+  static constexpr uint32_t kIdS = idesc_bf16_f32(128, 256, 0, 0), kIdO = idesc_bf16_f32(128, 256, 0, 1);
+  Smem<kSplit>& sm;
+  const uint32_t tmem;
+  const uint64_t wns;
+  const int lane;
+  const uint64_t qd, pd, kd, vd;
+  int sl = 0, ph = 0, nq = 0;
+  __device__ Issuer(Smem<kSplit>& s, uint32_t t, uint64_t w, int ln)
+      : sm(s), tmem(t), wns(w), lane(ln), qd(kmajor(s.q)), pd(kmajor(s.p)), kd(kmajor(s.ring)),
+        // values as the MN-major operand: 64-column slabs 8 KiB apart, 8-token groups 1 KiB apart
+        vd(smem_desc(smem_u32(s.ring), kSlab, 1024, kSwizzle128B)) {}
+  __device__ void step() {
+    if (++sl == G::kSlots) {
+      sl = 0;
+      ph ^= 1;
+    }
+  }
+  __device__ bool scores(int i, bool first, bool last) {
+    if (first && !warp_wait(&sm.q_full, nq++ & 1, 50, wns, lane)) return false;
+    const uint32_t d = tmem + kTmemS + 128 * (i & 1);
+#pragma unroll
+    for (int e = 0; e < kSlabs; ++e, step()) {
+      if (!warp_wait(&sm.full[sl], ph, 51, wns, lane)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t a = qd + e * (kSlab >> 4), b = kd + (uint32_t)sl * (G::kSlot >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_ss_pair(d, a + 2 * k, b + 2 * k, kIdS, (e | k) ? 1u : 0u);
+        if (kSplit) {
+          const uint64_t al = b + (kKvSlot >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_ss_pair(d, al + 2 * k, b + 2 * k, kIdS, 1u);
+        }
+        mma_commit_pair(&sm.empty[sl], kBoth);
+        if (e == kSlabs - 1) {
+          mma_commit_pair(&sm.s_full[i & 1], kBoth);
+          if (last) mma_commit_pair(&sm.q_empty, kBoth);
+        }
+      }
+      __syncwarp();
+    }
+    return true;
+  }
+  // P V of tile i of n items; `first`: it begins its token's output
+  __device__ bool values(int i, int n, bool first) {
+    if (!warp_wait(&sm.p_full, i & 1, 52, wns, lane)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int q = 0; q < kTilePages; ++q) {
+      if (q >= n) break;
+#pragma unroll
+      for (int j = 0; j < 2; ++j, step()) {
+        if (!warp_wait(&sm.full[sl], ph, 53, wns, lane)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t a = pd + q * (kSlab >> 4), b = vd + (uint32_t)sl * (G::kSlot >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss_pair(tmem + kTmemO + 128 * j, a + 2 * k, b + 128 * k, kIdO, (first && q == 0 && k == 0) ? 0u : 1u);
+          mma_commit_pair(&sm.empty[sl], kBoth);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) mma_commit_pair(&sm.pv_done, kBoth);
+    __syncwarp();
+    return true;
+  }
+};
+
+template <bool kSplit>
+__device__ void mma_role(Smem<kSplit>& sm, uint32_t tmem, const Params& p, int lane) {
+  Issuer<kSplit> is(sm, tmem, p.wait_ns, lane);
+  int i = 0, n_prev = 0;
+  bool ok = true, first_prev = false;
+  for (Walk w(p.q, sm.from, sm.to); ok && w.valid(); w.next()) {
+    const int nt = w.tiles(), n = w.k1 - w.at.k;
+    for (int t = 0; ok && t < nt; ++t, ++i) {
+      ok = is.scores(i, t == 0, t == nt - 1) && (i == 0 || is.values(i - 1, n_prev, first_prev)) && !aborted(sm);
+      n_prev = min(kTilePages, n - t * kTilePages);
+      first_prev = t == 0;
+    }
+  }
+  if (ok && i > 0) ok = is.values(i - 1, n_prev, first_prev);
+  if (!ok) set_abort(sm);
+  if (lane == 0) mma_commit_pair(&sm.fin, 1);
+  warp_wait(&sm.fin, 0, 54, p.wait_ns, lane);
+}
+
+// ---------------------------------------------------------------- softmax and output
+template <bool kSplit>
+struct Softmax {
+  Smem<kSplit>& sm;
+  const Params& p;
+  const uint32_t tl;               // this warp's TMEM lane quarter
+  const int lane, l, half, ch, head;
+  int worker;
+  int n_out = 0;                   // pieces written (parity of lbar)
+
+  // The finished piece's output: row sums of the head's four threads, then O / l.
+  __device__ bool finish(float lsum, float m, int tok, bool whole, int slot, int last_tile) {
+    float(&xl)[2][128] = sm.xl[n_out & 1];
+    xl[ch][l] = lsum;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.lbar);
+    if (!warp_wait(&sm.lbar, n_out & 1, 60, p.wait_ns, lane)) return false;
+    // the same order of additions in all four threads of the head
+    const int l0 = l & 63;
+    const float tot = (xl[0][l0] + xl[1][l0]) + (xl[0][l0 + 64] + xl[1][l0 + 64]);
+    if (!warp_wait(&sm.pv_done, last_tile & 1, 61, p.wait_ns, lane)) return false;
+    tc_fence_after();
+    ++n_out;
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;  // no visible row: zero (a NaN sum stays NaN)
+    const float lse = tot == 0.f ? -INFINITY : m + log2f(tot);
+    const int col = 256 * ch + 128 * half;  // this thread's 128 latent columns
+    if (half == 0 && ch == 0) {
+      if (!whole) p.part_lse[(long long)slot * kH + head] = lse;
+      else if (p.lse != nullptr) p.lse[(long long)tok * kH + head] = lse;
+    }
+    bf16* out = p.o_lat + ((long long)tok * kH + head) * kDc + col;
+    float* part = p.part_o + ((long long)slot * kH + head) * kDc + col;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      tmem_ld32(tl + kTmemO + 128 * ch + 32 * c, o);
+      tmem_wait_ld();
+      const float* f = reinterpret_cast<const float*>(o);
+      if (whole) {
+        uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          dst[k] = make_uint4(pack_bf16x2(f[8 * k] * inv, f[8 * k + 1] * inv), pack_bf16x2(f[8 * k + 2] * inv, f[8 * k + 3] * inv),
+                              pack_bf16x2(f[8 * k + 4] * inv, f[8 * k + 5] * inv), pack_bf16x2(f[8 * k + 6] * inv, f[8 * k + 7] * inv));
+      } else {
+        float4* dst = reinterpret_cast<float4*>(part + 32 * c);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          dst[k] = make_float4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
+      }
+    }
+    tc_fence_before();
+    return true;
+  }
+
+  // A token that sees nothing: zeros, log-sum-exp of an empty set.
+  __device__ void write_empty(int tok) {
+    uint4* dst = reinterpret_cast<uint4*>(p.o_lat + ((long long)tok * kH + head) * kDc + 256 * ch + 128 * half);
+#pragma unroll 1
+    for (int k = 0; k < 16; ++k) dst[k] = make_uint4(0, 0, 0, 0);
+    if (half == 0 && ch == 0 && p.lse != nullptr) p.lse[(long long)tok * kH + head] = -INFINITY;
+  }
+
+  __device__ bool run(const Place& from, const Place& to) {
+    float m_used = -INFINITY, lsum = 0.f;
+    // the piece whose output is still in TMEM
+    bool open = false, open_whole = false;
+    int open_tok = 0, open_slot = 0, i = 0;
+    for (Walk w(p.q, from, to); w.valid(); w.next()) {
+      const int nt = w.tiles();
+      if (nt == 0) {
+        write_empty(w.token());
+        continue;
+      }
+      for (int t = 0; t < nt; ++t, ++i) {
+        // this thread's item: which of the tile's rows are visible
+        const int k = w.at.k + t * kTilePages + 2 * half + ch;
+        int lo = kPage, hi = kPage;
+        if (k < w.k1) {
+          const Item it = item_of(p.q.vis, w.position(), k);
+          const int phys = p.block_table[(long long)w.at.b * p.max_blocks + it.page];
+          if (phys >= 0 && phys < p.num_blocks) {
+            lo = it.a == 0 ? kPage - it.b : 0;  // as the loads shift them
+            hi = it.a == 0 ? kPage : it.b - it.a;
+          } else if (lane == 0) {
+            report(MLA_ERR_BOUNDS, 22, w.at.b, phys);
+          }
+        }
+        if (!warp_wait(&sm.s_full[i & 1], (i >> 1) & 1, 62, p.wait_ns, lane)) return false;
+        tc_fence_after();
+        float s[64];
+        {
+          uint32_t a[32], b[32];
+          const uint32_t at = tl + kTmemS + 128 * (i & 1) + 64 * ch;
+          tmem_ld32(at, a);
+          tmem_ld32(at + 32, b);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            s[c] = __uint_as_float(a[c]);
+            s[32 + c] = __uint_as_float(b[c]);
+          }
+        }
+        tc_fence_before();
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          s[c] = c >= lo && c < hi ? s[c] * p.scale_log2 : -INFINITY;
+          mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+        }
+        sm.xm[i & 1][ch][l] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.xbar[i & 1]);
+        if (!warp_wait(&sm.xbar[i & 1], (i >> 1) & 1, 63, p.wait_ns, lane)) return false;
+        const float m_tile = fmaxf(fmaxf(sm.xm[i & 1][0][l], sm.xm[i & 1][1][l]),
+                                   fmaxf(sm.xm[i & 1][0][l ^ 64], sm.xm[i & 1][1][l ^ 64]));
+        const bool first = t == 0;
+        const float m_prev = m_used, l_prev = lsum;  // of the open piece, when this tile begins another
+        if (first) {
+          m_used = -INFINITY;
+          lsum = 0.f;
+        }
+        // rescale only when P could grow past 2^8: P and O are exact in the scale
+        float alpha = 1.f;
+        const bool rescale = m_tile > m_used + kRescaleLog2;
+        if (rescale) {
+          alpha = exp2_fast(m_used - m_tile);  // 0 at the piece's first finite maximum
+          m_used = m_tile;
+        }
+        const float base = m_used == -INFINITY ? 0.f : m_used;
+        uint32_t pk[32];
+        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float p0 = exp2_fast(s[2 * c] - base), p1 = exp2_fast(s[2 * c + 1] - base);
+          ps[c & 3] += p0 + p1;
+          pk[c] = pack_bf16x2(p0, p1);
+        }
+        lsum = lsum * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+
+        // P V of the tile before reads P and adds to O: it must be over before
+        // this tile writes P, rescales O or hands O to the next token.
+        if (first && open) {
+          if (!finish(l_prev, m_prev, open_tok, open_whole, open_slot, i - 1)) return false;
+        } else if (i >= 1) {
+          if (!warp_wait(&sm.pv_done, (i - 1) & 1, 64, p.wait_ns, lane)) return false;
+          tc_fence_after();
+        }
+        if (!first && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            const uint32_t a = tl + kTmemO + 128 * ch + 32 * c;
+            tmem_ld32(a, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(a, o);
+          }
+          tmem_wait_st();
+        }
+        // row hl of the item's P slab, K-major with the 128-byte swizzle
+        const int hl = l & 63;
+        uint8_t* row = sm.p[2 * half + ch] + hl * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(row + ((c ^ (hl & 7)) << 4)) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(leader(&sm.p_full));
+      }
+      open = true;
+      open_whole = w.whole();
+      open_tok = w.token();
+      open_slot = 2 * worker + (w.at.k > 0 ? 0 : 1);
+    }
+    return !open || finish(lsum, m_used, open_tok, open_whole, open_slot, i - 1);
+  }
+};
+
+// ---------------------------------------------------------------- kernel
+template <bool kSplit, typename Maps>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    chunk_pair_kernel(const __grid_constant__ Maps pool, const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ CUtensorMap qlomap, const __grid_constant__ Params p) {
+  using G = Geo<kSplit>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<kSplit>& sm =
+      *reinterpret_cast<Smem<kSplit>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = uni(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank(), worker = blockIdx.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G::kSlots; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.s_full[b], 1);
+      mbar_init(&sm.xbar[b], kSoftmaxWarps);
+    }
+    mbar_init(&sm.p_full, 2 * kSoftmaxWarps);
+    mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.lbar, kSoftmaxWarps);
+    mbar_init(&sm.fin, 1);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(&sm.tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (warp == kQueryWarp && lane == 0) {
+    prefetch_tensormap(&pool.end[sizeof(Maps) / sizeof(CUtensorMap) - 1]);
+    prefetch_tensormap(&qmap);
+  }
+  pdl_wait();  // the queries, the tables and the appended rows come from the kernels before
+  pdl_trigger();
+  find_range(sm, p, worker);
+  fence_proxy_async_smem();  // the prefix sums give way to the ring's loads
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised, their prefix sums read
+  tc_fence_after();
+  const uint32_t tmem = uni(sm.tmem_base);
+  const Place from = sm.from, to = sm.to;
+
+  if (rank == 0 && threadIdx.x == 0) {
+    const Shares e = shares_of(p.q, from, to);
+    p.piece[worker] = make_int4(e.x, e.y, e.z, 0);
+  }
+
+  if (warp < kSoftmaxWarps) {
+    const int l = (warp & 3) * 32 + lane;
+    Softmax<kSplit> so{sm, p, tmem + ((uint32_t)((warp & 3) * 32) << 16), lane, l, l >> 6, warp >> 2,
+                       kHalfH * rank + (l & 63), worker};
+    if (!so.run(from, to)) set_abort(sm);
+  } else if (warp == kMmaWarp) {
+    if (rank == 0) mma_role(sm, tmem, p, lane);
+  } else if (warp == kQueryWarp) {
+    query_role(sm, &qmap, p, rank, lane);
+  } else {
+    load_role<kSplit, Maps>(sm, pool, &qlomap, p, warp - kLoadWarp0, rank, lane);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's MMAs and remote arrives are over before TMEM and shared memory go away
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- merge
+// Joins the pieces of the tokens that several workers share:
+//   o_lat = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).
+// Grid (workers, head groups): block (w, y) joins the token that worker w
+// begins and does not end; most workers have none.  Pieces are summed in the
+// order of the workers.  A thread owns 8 latent columns of one head.
+constexpr int kMergeHeads = 4;
+__global__ void __launch_bounds__(256) chunk_merge_kernel(int workers, const int4* __restrict__ piece,
+                                                          const float* __restrict__ part_lse,
+                                                          const float* __restrict__ part_o, bf16* __restrict__ o_lat,
+                                                          float* __restrict__ lse_out) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ int slots[kMaxWorkers + 1];
+  __shared__ int count;
+  const int w0 = blockIdx.x, tok = piece[w0].z;
+  if (tok < 0) return;
+  if (threadIdx.x < 32) {  // the workers behind w0 that go on with the token, up to the one that ends it
+    const int lane = threadIdx.x;
+    int n = 1;
+    if (lane == 0) slots[0] = 2 * w0 + 1;
+    for (int b = w0 + 1; b < workers; b += 32) {
+      const int4 e = b + lane < workers ? piece[b + lane] : make_int4(-1, 0, -1, 0);
+      const unsigned on = __ballot_sync(0xffffffffu, e.x == tok), end = __ballot_sync(0xffffffffu, e.x == tok && e.y);
+      if (e.x == tok) slots[n + __popc(on & ((1u << lane) - 1))] = 2 * (b + lane);
+      n += __popc(on);
+      if (end) break;
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int n = count;
+  const int h = blockIdx.y * kMergeHeads + threadIdx.x / 64, d = 8 * (threadIdx.x % 64);
+  float M = -INFINITY, Z = 0.f;
+  bool nan = false;  // a maximum passes over NaN, the result must not
+  for (int i = 0; i < n; ++i) {
+    const float x = part_lse[(long long)slots[i] * kH + h];
+    M = fmaxf(M, x);
+    nan |= x != x;
+  }
+  if (nan) Z = NAN;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (M != -INFINITY) {  // else no piece has a visible row
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wt = exp2f(part_lse[(long long)slots[i] * kH + h] - M);
+      const float4* src = reinterpret_cast<const float4*>(part_o + ((long long)slots[i] * kH + h) * kDc + d);
+      const float4 x = __ldcs(src), y = __ldcs(src + 1);
+      Z += wt;
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = fmaf(wt, v[k], acc[k]);
+    }
+  }
+  const float inv = Z == 0.f ? 0.f : 1.f / Z;
+  *reinterpret_cast<uint4*>(o_lat + ((long long)tok * kH + h) * kDc + d) =
+      make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                 pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+  if (lse_out != nullptr && d == 0) lse_out[(long long)tok * kH + h] = Z == 0.f ? -INFINITY : M + log2f(Z);
+}
+
+// ================================================================ host side
+// The pool as pairdec::pool_map has it, ending at row `rows` of every page: the
+// rows behind it read as zeros like those outside the page.
+inline mla_status pool_map(const mla_cache* k, CUtensorMap* map, int rows) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) return MLA_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)kRow, (cuuint64_t)rows, (cuuint64_t)k->num_blocks};
+  const cuuint64_t strides[2] = {(cuuint64_t)kRow * 2, (cuuint64_t)kRow * 2 * kPage};
+  const cuuint32_t box[3] = {64, (cuuint32_t)kPage, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k->pool, dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace chunk
+}  // namespace mla

@@ -1,0 +1,244 @@
+// What the new tokens of a ragged batch see, and how that work is cut among
+// the workers of the tensor-core kernel.
+//
+// Sequence b has the n_b = cu_q[b + 1] - cu_q[b] query rows (tokens)
+// t = cu_q[b] + j and seq_lens[b] cached rows, its new ones included, so
+// token t stands at position p = seq_lens[b] - n_b + j and sees
+//   rows u <= p                                            (window = 0)
+//   rows u <= p with u > p - window or u < n_sinks         (window > 0).
+// The visible rows are walked page by page.  Item k of a token is a page and
+// the range [a, b) of its rows that are visible: the sink pages first, then
+// the pages of the window; while the window still touches the sinks the two
+// are one run from row 0.  A page that holds both the end of the sinks and the
+// start of the window is two items.  Page order does not matter to a softmax.
+//
+// The number of items of a token is a sum of floors of its position, so the
+// items of a whole run of tokens have a closed form, and the cut of all work
+// into equal parts needs one prefix sum over the sequences, not over the
+// tokens: every CTA makes it for itself (8 bytes read per sequence) and there
+// is no planning launch ahead of the attention.
+#pragma once
+
+#include "common.cuh"
+
+namespace mla {
+namespace chunk {
+
+constexpr int kPage = 64;
+constexpr int kMaxBatch = 8192;   // sequences of a call: their prefix sums sit in shared memory
+constexpr int kTilePages = 4;     // items of a tile of the tensor-core kernel
+// A token's fixed cost in items: its query load and epilogue, and the unused
+// part of its last tile.
+constexpr int kTokenCost = 3;
+
+struct Visible {
+  int window, sinks;  // window = 0: all rows up to the token's own
+
+  // first window row of a token at position p, 0 while the window touches the sinks
+  __host__ __device__ int start(int p) const {
+    if (window == 0) return 0;
+    const int w0 = p - window + 1;  // p >= 0, window >= 1: no overflow
+    return w0 <= sinks ? 0 : w0;
+  }
+  __host__ __device__ int sink_items() const { return sinks / kPage + (sinks % kPage != 0); }
+  __host__ __device__ int items(int p) const {
+    const int w0 = start(p);
+    return (w0 > 0 ? sink_items() : 0) + p / kPage - w0 / kPage + 1;
+  }
+  // sum over p < n of floor(p / 64)
+  __host__ __device__ static long long floors(long long n) {
+    const long long q = n / kPage, r = n % kPage;
+    return kPage * (q * (q - 1) / 2) + q * r;
+  }
+  // items of the tokens at positions p0 .. p0 + n - 1
+  __host__ __device__ long long items_of_run(long long p0, long long n) const {
+    long long s = n + floors(p0 + n) - floors(p0);
+    if (window > 0) {
+      const long long lone = (long long)sinks + window;  // first position whose window is apart from the sinks
+      const long long f = p0 > lone ? p0 : lone;
+      if (f < p0 + n) {
+        const long long m = p0 + n - f;
+        s += m * sink_items() - (floors(p0 + n - window + 1) - floors(f - window + 1));
+      }
+    }
+    return s;
+  }
+};
+
+// Item k of the token at position p: page, visible rows [a, b) of it.
+struct Item {
+  int page, a, b;
+};
+__host__ __device__ inline Item item_of(const Visible& vis, int p, int k) {
+  const int w0 = vis.start(p);
+  const int ns = w0 > 0 ? vis.sink_items() : 0;
+  Item it;
+  if (k < ns) {
+    it.page = k;
+    it.a = 0;
+    it.b = vis.sinks - k * kPage < kPage ? vis.sinks - k * kPage : kPage;
+  } else {
+    it.page = w0 / kPage + (k - ns);
+    it.a = w0 - it.page * kPage > 0 ? w0 - it.page * kPage : 0;
+    it.b = p + 1 - it.page * kPage < kPage ? p + 1 - it.page * kPage : kPage;
+  }
+  return it;
+}
+
+// A ragged batch and what its tokens see.
+struct Batch {
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  int batch, n_tok, max_rows;  // max_rows: what a block table row holds
+  Visible vis;
+};
+
+// The query rows of one sequence: tokens [t0, t0 + n) at positions p0 + j.
+// p0 < 0: its tokens see nothing.
+struct Sequence {
+  int t0, n, p0;
+  enum { kFine, kBadRows, kBadLength } state;
+};
+
+// Sequence b, its lengths checked; a sequence whose entries do not fit has no
+// tokens (cu_q out of order or past n_tok) or tokens that see nothing (no
+// cached rows, or a length that does not hold them).
+__host__ __device__ inline Sequence sequence_of(const Batch& q, int b) {
+  Sequence s;
+  const int lo = q.cu_q[b], hi = q.cu_q[b + 1], len = q.seq_lens[b];
+  s.t0 = lo;
+  s.n = hi - lo;
+  s.p0 = len - s.n;
+  s.state = Sequence::kFine;
+  if (lo < 0 || hi < lo || hi > q.n_tok || (b == 0 && lo != 0)) {
+    s.t0 = s.n = 0;
+    s.p0 = -1;
+    s.state = Sequence::kBadRows;
+  } else if (s.n > 0 && (len < s.n || len > q.max_rows)) {
+    s.p0 = -1;
+    if (len != 0) s.state = Sequence::kBadLength;
+  }
+  return s;
+}
+
+__device__ __forceinline__ void report_sequence(const Batch& q, int b, const Sequence& s) {
+  if (s.state == Sequence::kBadRows) report(MLA_ERR_BOUNDS, 20, b, q.cu_q[b + 1]);
+  if (s.state == Sequence::kBadLength) report(MLA_ERR_BOUNDS, 21, b, q.seq_lens[b]);
+}
+
+// Cost of the first n tokens of a sequence.
+__host__ __device__ inline long long cost_of_tokens(const Visible& vis, const Sequence& s, int n) {
+  return (long long)kTokenCost * n + (s.p0 >= 0 ? vis.items_of_run(s.p0, n) : 0);
+}
+
+// A place in the order of all items: sequence, token within it, item.
+struct Place {
+  int b, j, k;
+};
+__host__ __device__ inline bool before(const Place& x, const Place& y) {
+  return x.b < y.b || (x.b == y.b && (x.j < y.j || (x.j == y.j && x.k < y.k)));
+}
+
+// The place at cost x, given the costs C[0 .. batch] of the sequences before
+// each.  Inside a token it is moved back to a tile boundary.
+__host__ __device__ inline Place place_at(const Batch& q, const long long* C, long long x) {
+  if (x >= C[q.batch]) return {q.batch, 0, 0};
+  int lo = 0, hi = q.batch - 1;  // the last sequence with C[b] <= x; it has tokens, as C[b + 1] > x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (C[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  const Sequence s = sequence_of(q, lo);
+  const long long r = x - C[lo];
+  int a = 0, z = s.n - 1;
+  while (a < z) {
+    const int mid = (a + z + 1) >> 1;
+    if (cost_of_tokens(q.vis, s, mid) <= r) a = mid; else z = mid - 1;
+  }
+  int k = 0;
+  if (s.p0 >= 0) {
+    const long long i = r - cost_of_tokens(q.vis, s, a) - kTokenCost;
+    const int n = q.vis.items(s.p0 + a);
+    k = i <= 0 ? 0 : (int)(i < n ? i : n - 1) / kTilePages * kTilePages;
+  }
+  return {lo, a, k};
+}
+
+// Where the range of worker w of `workers` begins (w = workers: where the last ends).
+__host__ __device__ inline Place cut(const Batch& q, const long long* C, int w, int workers) {
+  const long long total = C[q.batch];
+  return place_at(q, C, total / workers * w + total % workers * w / workers);
+}
+
+// A value that all lanes of a warp hold, in the warp-uniform datapath.
+__host__ __device__ __forceinline__ int uni(int x) {
+#ifdef __CUDA_ARCH__
+  return __shfl_sync(0xffffffffu, x, 0);
+#else
+  return x;
+#endif
+}
+
+// The pieces of a range in order: a piece is a run of items [at.k, k1) of one
+// token (no items for a token that sees nothing).  Whole warps.
+struct Walk {
+  const Batch& q;
+  Place at, to;
+  Sequence s;
+  int n_items, k1;  // items of the token; end of the piece
+  __host__ __device__ Walk(const Batch& q_, Place from, Place to_) : q(q_), at(from), to(to_), n_items(0), k1(0) {
+    s.n = 0;
+    if (!valid()) return;
+    load();
+    settle();
+  }
+  __host__ __device__ bool valid() const { return before(at, to); }
+  __host__ __device__ void load() {
+    s = sequence_of(q, at.b);
+    s.t0 = uni(s.t0);
+    s.n = uni(s.n);
+    s.p0 = uni(s.p0);
+  }
+  // bring `at` to a token that exists, and measure its piece
+  __host__ __device__ void settle() {
+    while (valid() && at.j >= s.n) {
+      at.j = 0;
+      at.k = 0;
+      if (++at.b >= q.batch) return;  // `to` is at most (batch, 0, 0): not valid any more
+      load();
+    }
+    if (!valid()) return;
+    n_items = s.p0 < 0 ? 0 : q.vis.items(s.p0 + at.j);
+    k1 = at.b == to.b && at.j == to.j ? (to.k < n_items ? to.k : n_items) : n_items;
+  }
+  __host__ __device__ void next() {
+    ++at.j;
+    at.k = 0;
+    settle();
+  }
+  __host__ __device__ int token() const { return s.t0 + at.j; }
+  __host__ __device__ int position() const { return s.p0 + at.j; }
+  __host__ __device__ bool whole() const { return at.k == 0 && k1 == n_items; }
+  __host__ __device__ int tiles() const { return (k1 - at.k + kTilePages - 1) / kTilePages; }
+};
+
+// What a worker holds of tokens that it does not hold whole: x = the token that
+// its range continues (-1: none), y = 1 if that token ends in its range, z = the
+// token that its range begins and does not end (-1: none).
+struct Shares {
+  int x, y, z;
+};
+__host__ __device__ inline Shares shares_of(const Batch& q, const Place& from, const Place& to) {
+  const bool same = from.b == to.b && from.j == to.j;
+  Shares e{-1, 0, -1};
+  if (!before(from, to)) return e;
+  if (from.k > 0) {
+    e.x = sequence_of(q, from.b).t0 + from.j;
+    e.y = same ? 0 : 1;
+  }
+  if (to.k > 0 && !(same && from.k > 0)) e.z = sequence_of(q, to.b).t0 + to.j;
+  return e;
+}
+
+}  // namespace chunk
+}  // namespace mla

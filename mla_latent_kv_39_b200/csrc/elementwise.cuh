@@ -45,16 +45,27 @@ __device__ __forceinline__ long long cache_row_slot(const int32_t* seq_idx, cons
   return (long long)phys * bs + (p % bs);
 }
 
+// The same for a call that gives each token's slot in the pool: -1 marks a
+// padding token, whose row is not stored; any other slot outside the pool
+// records a bounds error.
+__device__ __forceinline__ long long given_row_slot(const long long* slots, int t, int num_blocks, int bs) {
+  const long long slot = slots[t];
+  if (slot >= -1 && slot < (long long)num_blocks * bs) return slot;
+  report(MLA_ERR_BOUNDS, 8, t, (int)(slot >> 32 == 0 ? slot : slot >> 32));
+  return -1;
+}
+
 // New latent rows from exact (fp64) projections C = x [W_DKV | W_KR] (the sum
 // of `splits` fp64 partials over K):
 // c = C[:, :d_c], k_R = RoPE(C[:, d_c:], pos); each value rounded once to T
-// and written to its paged slot.  One thread per latent value or rotary pair.
+// and written to its paged slot (from the block table, or `slots` where that is
+// not null).  One thread per latent value or rotary pair.
 template <typename T>
 __global__ void append_finish_kernel(const double* __restrict__ C, int splits, int n_tok, int d_c, int d_r,
                                      double theta, const int32_t* __restrict__ seq_idx,
                                      const int32_t* __restrict__ pos, T* __restrict__ pool,
                                      const int32_t* __restrict__ block_table, int batch,
-                                     int max_blocks, int num_blocks, int bs) {
+                                     int max_blocks, int num_blocks, int bs, const long long* __restrict__ slots) {
   pdl_wait();
   pdl_trigger();
   const int per_tok = d_c + d_r / 2;
@@ -62,7 +73,9 @@ __global__ void append_finish_kernel(const double* __restrict__ C, int splits, i
   for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
        i += (long long)gridDim.x * blockDim.x) {
     const int t = (int)(i / per_tok), k = (int)(i % per_tok);
-    const long long slot = cache_row_slot(seq_idx, pos, t, block_table, batch, max_blocks, num_blocks, bs);
+    const long long slot = slots != nullptr
+                               ? given_row_slot(slots, t, num_blocks, bs)
+                               : cache_row_slot(seq_idx, pos, t, block_table, batch, max_blocks, num_blocks, bs);
     if (slot < 0) continue;
     const int row = d_c + d_r;
     const long long split_stride = (long long)n_tok * row;
@@ -95,7 +108,8 @@ __global__ void append_finish_kernel(const double* __restrict__ C, int splits, i
 __global__ void __launch_bounds__(256) append_finish_fp8_kernel(
     const double* __restrict__ C, int n_tok, int d_c, int d_r, double theta, const int32_t* __restrict__ seq_idx,
     const int32_t* __restrict__ pos, __nv_fp8_e4m3* __restrict__ pool, float* __restrict__ row_scale,
-    const int32_t* __restrict__ block_table, int batch, int max_blocks, int num_blocks, int bs) {
+    const int32_t* __restrict__ block_table, int batch, int max_blocks, int num_blocks, int bs,
+    const long long* __restrict__ slots) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ double v[];  // [d_c + d_r]
@@ -103,7 +117,9 @@ __global__ void __launch_bounds__(256) append_finish_fp8_kernel(
   __shared__ long long slot_s;
   const int t = blockIdx.x, row = d_c + d_r;
   if (t >= n_tok) return;
-  if (threadIdx.x == 0) slot_s = cache_row_slot(seq_idx, pos, t, block_table, batch, max_blocks, num_blocks, bs);
+  if (threadIdx.x == 0)
+    slot_s = slots != nullptr ? given_row_slot(slots, t, num_blocks, bs)
+                              : cache_row_slot(seq_idx, pos, t, block_table, batch, max_blocks, num_blocks, bs);
   const double* src = C + (long long)t * row;
   for (int k = threadIdx.x; k < d_c + d_r / 2; k += blockDim.x) {
     if (k < d_c) {

@@ -7,6 +7,10 @@
 #include <mutex>
 
 #include "append_f64.cuh"
+#include "batch_tables.cuh"
+#include "chunk_pair.cuh"
+#include "chunk_plan.cuh"
+#include "chunk_simt.cuh"
 #include "common.cuh"
 #include "decode_plan.cuh"
 #include "decode_simt.cuh"
@@ -59,6 +63,11 @@ inline bool all_aligned16(const P*... p) {
   return (aligned16(p) && ...);
 }
 
+template <typename... P>
+inline bool aligned4(const P*... p) {
+  return (((reinterpret_cast<uintptr_t>(p) & 3u) == 0) && ...);
+}
+
 inline mla_status st(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
 #define MLA_TRY(expr)                          \
@@ -97,7 +106,7 @@ size_t append_ws(const mla_config* c, int n_tok) {
 template <typename T>
 mla_status append_impl(const mla_config* c, const void* x, int n, const void* W_DKV, const void* W_KR,
                        const int32_t* seq_idx, const int32_t* pos, const mla_cache* k, void* ws,
-                       cudaStream_t s) {
+                       cudaStream_t s, const long long* slots = nullptr) {
   const int row = c->d_c + c->d_r;
   double* C = static_cast<double*>(ws);
   MLA_CUDA(cudaMemsetAsync(C, 0, sizeof(double) * (size_t)n * row, s));
@@ -121,12 +130,12 @@ mla_status append_impl(const mla_config* c, const void* x, int n, const void* W_
     if (smem > 48 * 1024) return MLA_ERR_UNSUPPORTED;
     return st(launch_chained(append_finish_fp8_kernel, dim3(n), dim3(256), smem, s, (const double*)C, n, c->d_c,
                              c->d_r, c->rope_theta, seq_idx, pos, static_cast<__nv_fp8_e4m3*>(k->pool), k->row_scale,
-                             k->block_table, k->batch, k->max_blocks_per_seq, k->num_blocks, c->block_size));
+                             k->block_table, k->batch, k->max_blocks_per_seq, k->num_blocks, c->block_size, slots));
   }
   const long long total = (long long)n * (c->d_c + c->d_r / 2);
   return st(launch_chained(append_finish_kernel<T>, dim3(grid_for(total)), dim3(256), 0, s, (const double*)C, 1, n,
                             c->d_c, c->d_r, c->rope_theta, seq_idx, pos, static_cast<T*>(k->pool), k->block_table,
-                            k->batch, k->max_blocks_per_seq, k->num_blocks, c->block_size));
+                            k->batch, k->max_blocks_per_seq, k->num_blocks, c->block_size, slots));
 }
 
 // ---------------------------------------------------------------- absorb
@@ -328,18 +337,23 @@ OutTcWs out_tc_ws(const mla_config* c, int n) {
   return w;
 }
 
-mla_status out_tc(const mla_config* c, const float* o_lat, int n, const void* W_UV, const void* W_O, void* y,
-                  void* ws, cudaStream_t s) {
+// o_lat in fp32, or already in bf16 (`stored`; o_lat is then null).
+mla_status out_tc(const mla_config* c, const float* o_lat, const bf16* stored, int n, const void* W_UV,
+                  const void* W_O, void* y, void* ws, cudaStream_t s) {
   const OutTcWs w = out_tc_ws(c, n);
   char* base = static_cast<char*>(ws);
   float* part = reinterpret_cast<float*>(base + w.part);
   bf16* ol = reinterpret_cast<bf16*>(base + w.ol);
   bf16* oh = reinterpret_cast<bf16*>(base + w.oh);
-  const long long cnt = (long long)n * c->n_heads * c->d_c;
-  MLA_CUDA(launch_chained(wg::split_bf16_kernel, dim3(grid_for(cnt / 4)), dim3(256), 0, s, o_lat, cnt, ol,
-                          (bf16*)nullptr));
+  const bf16* in = stored;
+  if (in == nullptr) {
+    const long long cnt = (long long)n * c->n_heads * c->d_c;
+    MLA_CUDA(launch_chained(wg::split_bf16_kernel, dim3(grid_for(cnt / 4)), dim3(256), 0, s, o_lat, cnt, ol,
+                            (bf16*)nullptr));
+    in = ol;
+  }
   const ProjSpecs ps = proj_specs(c, n, false, nullptr, nullptr, nullptr, W_UV, W_O, nullptr, nullptr, nullptr,
-                                  nullptr, nullptr, ol, oh);
+                                  nullptr, nullptr, in, oh);
   MLA_TRY(wg::run(ps.uv, part, nullptr, oh, nullptr, s));
   return wg::run(ps.o, part, nullptr, static_cast<bf16*>(y), nullptr, s);
 }
@@ -436,6 +450,133 @@ __global__ void wait_timeout_check_kernel(unsigned long long limit_ns) {
     sm100::mbar_arrive(&bar);  // the second arrival never comes
     sm100::mbar_wait(&bar, 0, 1, limit_ns);
   }
+}
+
+// ---------------------------------------------------------------- ragged chunks
+// Whether the tensor-core kernel takes the configuration (otherwise the CUDA-core one).
+bool chunk_tc(const mla_config* c) { return tc_decode(c) && pairdec::supports(c); }
+
+int chunk_workers(int max_workers) {
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  const int most = std::min(std::max(1, sms / 2), chunk::kMaxWorkers);
+  return max_workers > 0 ? std::min(max_workers, most) : most;
+}
+
+template <bool kSplit, typename Maps>
+mla_status chunk_pair_launch(const Maps& pool, const CUtensorMap& q, const CUtensorMap& qlo, const chunk::Params& p,
+                             cudaStream_t s) {
+  static std::atomic<uint64_t> attr{0};
+  constexpr size_t smem = chunk::smem_bytes<kSplit>();
+  MLA_TRY(pairdec::set_smem_once((const void*)chunk::chunk_pair_kernel<kSplit, Maps>, smem, attr));
+  return st(launch_chained(chunk::chunk_pair_kernel<kSplit, Maps>, dim3(2 * p.workers), dim3(chunk::kThreads), smem, s,
+                           pool, q, qlo, p));
+}
+
+template <typename Maps>
+mla_status chunk_pool_maps(const mla_cache* k, Maps* maps) {
+  constexpr int n = sizeof(Maps) / sizeof(CUtensorMap);
+  for (int i = 0; i < n; ++i) MLA_TRY(chunk::pool_map(k, &maps->end[i], n == 1 ? chunk::kPage : i + 1));
+  return MLA_OK;
+}
+
+mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch& b, const mla_cache* k, int workers,
+                         bf16* o_lat, float* lse, void* ws, cudaStream_t s) {
+  const bool split = (c->flags & MLA_FLAG_SPLIT_QUERY) != 0;
+  const chunk::Layout L = chunk::layout(workers);
+  char* base = static_cast<char*>(ws);
+  const chunk::Params p{b, k->block_table, k->max_blocks_per_seq, k->num_blocks, scale_of(c) * 1.4426950408889634f, g_wait_limit_ns.load(std::memory_order_relaxed), workers,
+                        reinterpret_cast<int4*>(base + L.off_piece), reinterpret_cast<float*>(base + L.off_lse),
+                        reinterpret_cast<float*>(base + L.off_o), o_lat, lse};
+  CUtensorMap qmap, qlo;
+  MLA_TRY(pairdec::query_map(q, b.n_tok, &qmap));
+  MLA_TRY(pairdec::query_map(split ? q + (long long)b.n_tok * chunk::kH * chunk::kRow : q, b.n_tok, &qlo));
+  // only a window shorter than a page cuts a page's rows on both sides
+  if (b.vis.window > 0 && b.vis.window < chunk::kPage) {
+    chunk::PoolMaps maps;
+    MLA_TRY(chunk_pool_maps(k, &maps));
+    MLA_TRY(split ? chunk_pair_launch<true>(maps, qmap, qlo, p, s) : chunk_pair_launch<false>(maps, qmap, qlo, p, s));
+  } else {
+    chunk::PoolMap map;
+    MLA_TRY(chunk_pool_maps(k, &map));
+    MLA_TRY(split ? chunk_pair_launch<true>(map, qmap, qlo, p, s) : chunk_pair_launch<false>(map, qmap, qlo, p, s));
+  }
+  return st(launch_chained(chunk::chunk_merge_kernel, dim3(workers, chunk::kH / chunk::kMergeHeads), dim3(256), 0, s,
+                           workers, (const int4*)p.piece, (const float*)p.part_lse, (const float*)p.part_o, o_lat, lse));
+}
+
+template <typename TQ, typename T, typename TO>
+mla_status chunk_simt_launch(const chunk::SimtArgs& a, cudaStream_t s) {
+  const int row = a.d_c + a.d_r;
+  const size_t smem = sizeof(float) * ((size_t)row + (size_t)chunk::kSimtWarps * a.d_c);
+  const dim3 grid(a.q.n_tok, a.H), block(32 * chunk::kSimtWarps);
+  if (a.d_c <= 64) return st(launch_chained(chunk::chunk_simt_kernel<TQ, T, TO, 2>, grid, block, smem, s, a));
+  if (a.d_c <= 512) return st(launch_chained(chunk::chunk_simt_kernel<TQ, T, TO, 16>, grid, block, smem, s, a));
+  if (row <= kSimtDecodeMaxRow) return st(launch_chained(chunk::chunk_simt_kernel<TQ, T, TO, 32>, grid, block, smem, s, a));
+  return MLA_ERR_UNSUPPORTED;
+}
+
+mla_status chunk_simt_impl(const mla_config* c, const void* q, const void* q_rope, const chunk::Batch& b,
+                           const mla_cache* k, void* o_lat, float* lse, cudaStream_t s) {
+  chunk::SimtArgs a{};
+  const int row = c->d_c + c->d_r;
+  if (row > kSimtDecodeMaxRow || c->n_heads > 65535) return MLA_ERR_UNSUPPORTED;
+  a.q_lat = q;
+  a.q_rope = q_rope;
+  a.q_stride = c->d_c;
+  a.qr_stride = c->d_r;
+  if (tc_decode(c)) {  // packed bf16 rows
+    const bf16* p = static_cast<const bf16*>(q);
+    a.q_rope = p + c->d_c;
+    a.q_stride = a.qr_stride = row;
+    if (c->flags & MLA_FLAG_SPLIT_QUERY) {
+      a.q_lo_lat = p + (long long)b.n_tok * c->n_heads * row;
+      a.q_lo_rope = static_cast<const bf16*>(a.q_lo_lat) + c->d_c;
+    }
+  }
+  a.pool = k->pool;
+  a.row_scale = fp8_cache(c) ? k->row_scale : nullptr;
+  a.block_table = k->block_table;
+  a.max_blocks = k->max_blocks_per_seq;
+  a.num_blocks = k->num_blocks;
+  a.bs = c->block_size;
+  a.q = b;
+  a.H = c->n_heads;
+  a.d_c = c->d_c;
+  a.d_r = c->d_r;
+  a.scale_log2 = scale_of(c) * 1.4426950408889634f;
+  a.o_lat = o_lat;
+  a.lse = lse;
+  if (fp8_cache(c)) return chunk_simt_launch<float, __nv_fp8_e4m3, bf16>(a, s);
+  if (c->dtype == MLA_BF16) return chunk_simt_launch<bf16, bf16, bf16>(a, s);
+  return chunk_simt_launch<float, float, float>(a, s);
+}
+
+mla_status chunk_impl(const mla_config* c, const void* q, const void* q_rope, int n_tok, const int32_t* cu_q, int batch,
+                      const mla_cache* k, const int32_t* seq_lens, const chunk::Visible& vis, int max_workers, void* o_lat,
+                      float* lse, void* ws, size_t ws_bytes, void* stream) {
+  MLA_TRY(check_cfg(c));
+  if (n_tok < 0 || batch < 0 || max_workers < 0) return MLA_ERR_INVALID_ARG;
+  if (n_tok == 0 || batch == 0) return MLA_OK;
+  if (!q || !cu_q || !seq_lens || !o_lat || !ws) return MLA_ERR_INVALID_ARG;
+  if (tc_decode(c) != (q_rope == nullptr)) return MLA_ERR_INVALID_ARG;  // packed bf16 rows, or two fp32 arrays
+  MLA_TRY(check_cache(c, k));
+  if (k->batch < batch) return MLA_ERR_INVALID_ARG;
+  if (batch > chunk::kMaxBatch) return MLA_ERR_UNSUPPORTED;
+  if (!aligned4(cu_q, seq_lens, k->block_table, lse)) return MLA_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const long long rows = (long long)k->max_blocks_per_seq * c->block_size;
+  const chunk::Batch b{cu_q, seq_lens, batch, n_tok, (int)std::min<long long>(rows, INT32_MAX - c->block_size), vis};
+  if (!chunk_tc(c)) {
+    const unsigned e = (unsigned)elem_bytes(c) - 1, eq = tc_decode(c) ? 1u : 3u, ep = fp8_cache(c) ? 0u : e;
+    if (((uintptr_t)q & eq) || ((uintptr_t)q_rope & eq) || ((uintptr_t)k->pool & ep) || ((uintptr_t)o_lat & e))
+      return MLA_ERR_INVALID_ARG;
+    return chunk_simt_impl(c, q, q_rope, b, k, o_lat, lse, s);
+  }
+  if ((long long)n_tok * chunk::kH > INT32_MAX) return MLA_ERR_UNSUPPORTED;  // a TMA coordinate
+  if (!all_aligned16(q, k->pool, o_lat, ws)) return MLA_ERR_INVALID_ARG;
+  const int workers = chunk_workers(max_workers);
+  if (ws_bytes < (size_t)chunk::layout(workers).total) return MLA_ERR_WORKSPACE;
+  return chunk_tc_impl(c, static_cast<const bf16*>(q), b, k, workers, static_cast<bf16*>(o_lat), lse, ws, s);
 }
 
 }  // namespace
@@ -770,10 +911,86 @@ mla_status mla_out_proj(const mla_config* cfg, const float* o_lat, int32_t n_tok
     if (!proj_tc_supported(cfg)) return MLA_ERR_UNSUPPORTED;
     if (!all_aligned16(o_lat, W_UV, W_O, y, workspace)) return MLA_ERR_INVALID_ARG;
     if (ws_bytes < out_tc_ws(cfg, n_tok).total) return MLA_ERR_WORKSPACE;
-    return out_tc(cfg, o_lat, n_tok, W_UV, W_O, y, workspace, s);
+    return out_tc(cfg, o_lat, nullptr, n_tok, W_UV, W_O, y, workspace, s);
   }
   if (ws_bytes < out_ws(cfg, n_tok).total) return MLA_ERR_WORKSPACE;
   return out_impl<float>(cfg, o_lat, n_tok, W_UV, W_O, y, workspace, s);
+}
+
+mla_status mla_out_proj_stored(const mla_config* cfg, const void* o_lat, int32_t n_tok, const void* W_UV,
+                               const void* W_O, void* y, void* workspace, size_t ws_bytes, void* stream) {
+  MLA_TRY(check_cfg(cfg));
+  if (cfg->dtype == MLA_F32)
+    return mla_out_proj(cfg, static_cast<const float*>(o_lat), n_tok, W_UV, W_O, y, workspace, ws_bytes, stream);
+  if (n_tok < 0) return MLA_ERR_INVALID_ARG;
+  if (n_tok == 0) return MLA_OK;
+  if (!o_lat || !W_UV || !W_O || !y || !workspace) return MLA_ERR_INVALID_ARG;
+  if (!proj_tc_supported(cfg)) return MLA_ERR_UNSUPPORTED;
+  if (!all_aligned16(o_lat, W_UV, W_O, y, workspace)) return MLA_ERR_INVALID_ARG;
+  if (ws_bytes < out_tc_ws(cfg, n_tok).total) return MLA_ERR_WORKSPACE;
+  return out_tc(cfg, nullptr, static_cast<const bf16*>(o_lat), n_tok, W_UV, W_O, y, workspace,
+                static_cast<cudaStream_t>(stream));
+}
+
+mla_status mla_batch_tables(const mla_config* cfg, int32_t batch, const int32_t* cached_lens, const int32_t* new_lens,
+                            const int32_t* free_blocks, int32_t n_free, const int32_t* free_head, int32_t num_blocks,
+                            int32_t* block_table, int32_t max_blocks_per_seq, int32_t n_tok, int32_t* cu_q,
+                            int32_t* seq_lens, int32_t* seq_idx, int32_t* pos, int64_t* slots, int32_t* free_head_out,
+                            void* stream) {
+  MLA_TRY(check_cfg(cfg));
+  if (batch < 0 || n_free < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || n_tok < 0) return MLA_ERR_INVALID_ARG;
+  if (batch == 0 && n_tok == 0) return MLA_OK;
+  if (batch == 0 || !cached_lens || !new_lens || !free_head || !block_table || !cu_q || !seq_lens || !free_head_out ||
+      (n_free > 0 && !free_blocks) || (n_tok > 0 && (!seq_idx || !pos || !slots)))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned4(cached_lens, new_lens, free_blocks, free_head, block_table, cu_q, seq_lens, seq_idx, pos, free_head_out) ||
+      ((uintptr_t)slots & 7u))
+    return MLA_ERR_INVALID_ARG;
+  if (batch > tables::kMaxBatch || (long long)max_blocks_per_seq * cfg->block_size > INT32_MAX - cfg->block_size)
+    return MLA_ERR_UNSUPPORTED;
+  const tables::Args a{batch, cfg->block_size, n_free, num_blocks, max_blocks_per_seq, n_tok, cached_lens, new_lens,
+                       free_blocks, free_head, block_table, cu_q, seq_lens, seq_idx, pos,
+                       reinterpret_cast<long long*>(slots), free_head_out};
+  return tables::launch(a, static_cast<cudaStream_t>(stream));
+}
+
+mla_status mla_cache_append_slots(const mla_config* cfg, const void* x, int32_t n_tok, const void* W_DKV,
+                                  const void* W_KR, const int32_t* pos, const int64_t* slots, const mla_cache* cache,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  MLA_TRY(check_cfg(cfg));
+  if (n_tok < 0) return MLA_ERR_INVALID_ARG;
+  if (n_tok == 0) return MLA_OK;
+  if (!x || !W_DKV || !W_KR || !pos || !slots || !workspace) return MLA_ERR_INVALID_ARG;
+  if (!aligned4(pos) || ((uintptr_t)slots & 7u)) return MLA_ERR_INVALID_ARG;
+  MLA_TRY(check_cache(cfg, cache));
+  if (ws_bytes < append_ws(cfg, n_tok)) return MLA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const long long* sl = reinterpret_cast<const long long*>(slots);
+  if (cfg->dtype == MLA_BF16)
+    return append_impl<bf16>(cfg, x, n_tok, W_DKV, W_KR, nullptr, pos, cache, workspace, s, sl);
+  return append_impl<float>(cfg, x, n_tok, W_DKV, W_KR, nullptr, pos, cache, workspace, s, sl);
+}
+
+size_t mla_chunk_workspace_size(const mla_config* cfg, int32_t n_tok, int32_t max_workers) {
+  if (check_cfg(cfg) != MLA_OK || n_tok < 0 || max_workers < 0) return 0;
+  return chunk_tc(cfg) ? (size_t)chunk::layout(chunk_workers(max_workers)).total : 256;
+}
+
+mla_status mla_chunk_attention(const mla_config* cfg, const void* q, const void* q_rope, int32_t n_tok,
+                               const int32_t* cu_q, int32_t batch, const mla_cache* cache, const int32_t* seq_lens,
+                               int32_t max_workers, void* o_lat, float* lse, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  return chunk_impl(cfg, q, q_rope, n_tok, cu_q, batch, cache, seq_lens, chunk::Visible{0, 0}, max_workers, o_lat, lse,
+                    workspace, ws_bytes, stream);
+}
+
+mla_status mla_window_attention(const mla_config* cfg, const void* q, const void* q_rope, int32_t n_tok,
+                                const int32_t* cu_q, int32_t batch, const mla_cache* cache, const int32_t* seq_lens,
+                                int32_t window, int32_t n_sinks, int32_t max_workers, void* o_lat, float* lse,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  if (window <= 0 || n_sinks < 0) return MLA_ERR_INVALID_ARG;
+  return chunk_impl(cfg, q, q_rope, n_tok, cu_q, batch, cache, seq_lens, chunk::Visible{window, n_sinks}, max_workers,
+                    o_lat, lse, workspace, ws_bytes, stream);
 }
 
 mla_status mla_check_wait_timeout(int64_t limit_ns, void* stream) {

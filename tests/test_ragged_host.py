@@ -1,0 +1,155 @@
+"""Ragged steps on a machine without a GPU: what a token sees and how the work
+is cut (the kernels' own index arithmetic, compiled for the host, against
+brute force), the reference's plan of a step, and the entry points' refusals."""
+
+import ctypes
+import random
+import subprocess
+from pathlib import Path
+
+import pytest
+
+from mla_latent_kv_39_b200 import abi, build
+
+ROOT = Path(__file__).resolve().parents[1]
+
+# Reads cases "window sinks batch n_tok max_rows workers, cu_q.., seq_lens.."
+# and prints for every worker its pieces: worker, sequence, token, position,
+# first item, end item, items of the token; then its shares; then, per token
+# with items, every item; and the closed-form item sums.
+PROGRAM = r'''
+#include <cstdio>
+#include <vector>
+#include "chunk_plan.cuh"
+using namespace mla::chunk;
+int main() {
+  int window, sinks, batch, n_tok, max_rows, workers;
+  while (std::scanf("%d %d %d %d %d %d", &window, &sinks, &batch, &n_tok, &max_rows, &workers) == 6) {
+    std::vector<int32_t> cu(batch + 1), len(batch);
+    for (auto& x : cu) std::scanf("%d", &x);
+    for (auto& x : len) std::scanf("%d", &x);
+    const Batch q{cu.data(), len.data(), batch, n_tok, max_rows, Visible{window, sinks}};
+    std::vector<long long> C(batch + 1, 0);
+    for (int b = 0; b < batch; ++b) {
+      const Sequence s = sequence_of(q, b);
+      C[b + 1] = C[b] + cost_of_tokens(q.vis, s, s.n);
+    }
+    std::printf("case %lld\n", C[batch]);
+    for (int w = 0; w < workers; ++w) {
+      const Place from = cut(q, C.data(), w, workers), to = cut(q, C.data(), w + 1, workers);
+      for (Walk k(q, from, to); k.valid(); k.next())
+        std::printf("piece %d %d %d %d %d %d %d %d\n", w, k.at.b, k.token(), k.position(), k.at.k, k.k1, k.n_items,
+                    (int)k.whole());
+      const Shares e = shares_of(q, from, to);
+      std::printf("shares %d %d %d %d\n", w, e.x, e.y, e.z);
+    }
+    for (int b = 0; b < batch; ++b) {
+      const Sequence s = sequence_of(q, b);
+      for (int j = 0; j < s.n && s.p0 >= 0; ++j) {
+        const int n = q.vis.items(s.p0 + j);
+        std::printf("token %d %d %d", b, s.t0 + j, n);
+        for (int i = 0; i < n; ++i) {
+          const Item it = item_of(q.vis, s.p0 + j, i);
+          std::printf(" %d %d %d", it.page, it.a, it.b);
+        }
+        std::printf("\n");
+      }
+    }
+  }
+}
+'''
+
+
+def visible_rows(p, window, sinks):
+    return [u for u in range(p + 1) if window == 0 or u > p - window or u < sinks]
+
+
+def make_cases():
+    r = random.Random(7)
+    cases = []
+    for _ in range(120):
+        window = r.choice([0, 0, 1, 2, 17, 62, 63, 64, 65, 100, 128, 300])
+        sinks = r.choice([0, 1, 4, 63, 64, 65, 130]) if window else 0
+        new = [r.choice([0, 1, 1, 2, 5, 40]) for _ in range(r.choice([1, 1, 2, 3, 9]))]
+        cached = [r.choice([0, 1, 63, 64, 65, 200, 700]) for _ in new]
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+        lens = [c + n for c, n in zip(cached, new)]
+        if r.random() < 0.2:
+            lens[r.randrange(len(lens))] = 0                      # an empty sequence
+        if r.random() < 0.1:
+            lens[-1] = 5000                                       # more rows than the table holds
+        n_tok = cu[-1] + r.choice([0, 3])
+        cases.append((window, sinks, cu, lens, n_tok, r.choice([1, 2, 7, 74])))
+    cases.append((0, 0, [0, 5, 3, 8], [5, 5, 5], 8, 4))           # prefix out of order
+    cases.append((0, 0, [0, 5, 30], [5, 25], 20, 4))              # past the token rows
+    cases.append((0, 0, [2, 5], [5], 5, 4))                       # not from 0
+    return cases
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    d = tmp_path_factory.mktemp("plan")
+    (d / "plan.cu").write_text(PROGRAM)
+    subprocess.run([build._nvcc(), *build.ARCH_FLAGS, "-std=c++17", f"-I{build.INCLUDE}", f"-I{build.CSRC}", "-o",
+                    str(d / "plan"), str(d / "plan.cu")], check=True, capture_output=True)
+    return d / "plan"
+
+
+def test_pieces_cover_every_visible_row_once(plan):
+    cases = make_cases()
+    text = "".join(f"{w} {s} {len(lens)} {n} 1024 {k} " + " ".join(map(str, cu + lens)) + "\n"
+                   for w, s, cu, lens, n, k in cases)
+    out = subprocess.run([str(plan)], input=text, capture_output=True, text=True, check=True).stdout
+    blocks = out.split("case ")[1:]
+    assert len(blocks) == len(cases)
+    for (window, sinks, cu, lens, n_tok, workers), block in zip(cases, blocks):
+        lines = block.splitlines()
+        total = int(lines[0])
+        pieces, shares, items = [], {}, {}
+        for ln in lines[1:]:
+            f = ln.split()
+            v = list(map(int, f[1:]))
+            if f[0] == "piece":
+                pieces.append(v)
+            elif f[0] == "shares":
+                shares[v[0]] = v[1:]
+            else:
+                items[v[0], v[1]] = [tuple(v[3 + 3 * i:6 + 3 * i]) for i in range(v[2])]
+        # the tokens that are to be computed, and what they see
+        want, cost = {}, 0
+        for b in range(len(lens)):
+            lo, hi, n = cu[b], cu[b + 1], cu[b + 1] - cu[b]
+            if lo < 0 or hi < lo or hi > n_tok or (b == 0 and lo):
+                continue
+            for j in range(n):
+                fine = n <= lens[b] <= 1024
+                want[(b, lo + j)] = visible_rows(lens[b] - n + j, window, sinks) if fine else []
+        for (b, t), rows in want.items():
+            its = items[b, t] if rows else []
+            got = [64 * page + u for page, a, e in its for u in range(a, e)]
+            assert sorted(got) == rows, (window, sinks, t)
+            assert all(0 <= a < e <= 64 for _, a, e in its)
+            if window == 0 or window >= 64:        # a range cut on both sides needs a window shorter than a page
+                assert all(a == 0 or e == 64 for _, a, e in its)
+            cost += 3 + len(its)
+        assert cost == total
+        # every token's items exactly once, in order over the workers; cuts on tile boundaries
+        seen = {}
+        for w, b, t, p, k0, k1, n, whole in pieces:
+            key = (b, t)
+            assert key in want and n == (len(items[key]) if want[key] else 0)
+            assert k0 == seen.get(key, (0, []))[0] and k0 % 4 == 0 and (k1 % 4 == 0 or k1 == n)
+            assert k1 > k0 or n == 0
+            assert bool(whole) == (k0 == 0 and k1 == n)
+            seen[key] = (k1, seen.get(key, (0, []))[1] + [(w, k0, k1)])
+        assert set(seen) == set(want)
+        for key, (end, parts) in seen.items():
+            assert end == (len(items[key]) if want[key] else 0)
+            if len(parts) > 1:   # the merge finds them: begun by one, continued and ended by the others
+                assert shares[parts[0][0]][2] == key[1]
+                for w, k0, k1 in parts[1:]:
+                    assert shares[w][0] == key[1] and shares[w][1] == (1 if w == parts[-1][0] else 0)
+        begun = sum(1 for v in shares.values() if v[2] >= 0)
+        assert begun == sum(1 for _, parts in seen.values() if len(parts) > 1)
