@@ -157,11 +157,22 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Lane 0 polls, the outcome is the warp's.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int where, uint64_t wns, int lane) {
-  int ok = 1;
-  if (lane == 0) ok = mbar_wait(bar, parity, where, wns) ? 1 : 0;
-  return uni(ok) != 0;
+// One lane of a converged warp, as a predicate that the compiler knows to hold
+// for a single lane: MMAs, commits and loads issued under it take their operands
+// from the uniform registers.  Issued under `lane == 0` the same instructions
+// went through per-lane moves: a tile of 68 MMAs with its 17 waits and commits
+// took 9,002 clocks, under elect 4,354, which is the pipe's own time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// All lanes of a converged warp wait; the outcome is the warp's.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int where, uint64_t wns) {
+  const bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, where, wns));
 }
 
 template <bool kSplit>
@@ -254,7 +265,8 @@ struct Loader {
   const Maps& pool;
   const CUtensorMap* qlo;
   const Params& p;
-  const int me, rank, lane;
+  const int me, rank;
+  const bool one;  // the issuing lane
   int sl = 0, use = 0, g = 0;  // ring slot, its use, running count
 
   __device__ bool mine() const { return (g & (kLoadWarps - 1)) == me; }
@@ -266,7 +278,7 @@ struct Loader {
     }
   }
   __device__ bool ready() {
-    return use == 0 || warp_wait(&sm.empty[sl], (use - 1) & 1, 40, p.wait_ns, lane);
+    return use == 0 || warp_wait(&sm.empty[sl], (use - 1) & 1, 40, p.wait_ns);
   }
   // the 9 key slabs of a tile of token `tok`
   __device__ bool keys(const TileLoad& t, int tok) {
@@ -274,7 +286,7 @@ struct Loader {
     for (int e = 0; e < kSlabs; ++e, step()) {
       if (!mine()) continue;
       if (!ready()) return false;
-      if (lane == 0) {
+      if (one) {
         const uint32_t bar = leader(&sm.full[sl]);
         if (rank == 0) mbar_arrive_expect_tx(&sm.full[sl], t.n * kSlab + (kSplit ? 2 * kSlab : 0));
 #pragma unroll
@@ -298,7 +310,7 @@ struct Loader {
       for (int j = 0; j < 2; ++j, step()) {
         if (!mine()) continue;
         if (!ready()) return false;
-        if (lane == 0) {
+        if (one) {
           const uint32_t bar = leader(&sm.full[sl]);
           if (rank == 0) mbar_arrive_expect_tx(&sm.full[sl], 2 * kKvSlot);
 #pragma unroll
@@ -316,7 +328,7 @@ struct Loader {
 template <bool kSplit, typename Maps>
 __device__ void load_role(Smem<kSplit>& sm, const Maps& pool, const CUtensorMap* qlo, const Params& p, int me, int rank,
                           int lane) {
-  Loader<kSplit, Maps> ld{sm, pool, qlo, p, me, rank, lane};
+  Loader<kSplit, Maps> ld{sm, pool, qlo, p, me, rank, elect_one()};
   TileLoad prev;
   prev.n = 0;
   bool ok = true;
@@ -333,15 +345,16 @@ __device__ void load_role(Smem<kSplit>& sm, const Maps& pool, const CUtensorMap*
 }
 
 template <bool kSplit>
-__device__ void query_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, int rank, int lane) {
+__device__ void query_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, int rank) {
+  const bool one = elect_one();
   int n = 0;
   for (Walk w(p.q, sm.from, sm.to); w.valid(); w.next()) {
     if (w.tiles() == 0) continue;
-    if (n >= 1 && !warp_wait(&sm.q_empty, (n - 1) & 1, 41, p.wait_ns, lane)) {
+    if (n >= 1 && !warp_wait(&sm.q_empty, (n - 1) & 1, 41, p.wait_ns)) {
       set_abort(sm);
       return;
     }
-    if (lane == 0) {
+    if (one) {
       if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kSlabs * kSlab);
       for (int e = 0; e < kSlabs; ++e)
         tma_load_2d_pair(sm.q[e], qmap, 64 * e, w.token() * kH + kHalfH * rank, leader(&sm.q_full));
@@ -359,11 +372,11 @@ struct Issuer {
   Smem<kSplit>& sm;
   const uint32_t tmem;
   const uint64_t wns;
-  const int lane;
+  const bool one;  // the issuing lane
   const uint64_t qd, pd, kd, vd;
   int sl = 0, ph = 0, nq = 0;
-  __device__ Issuer(Smem<kSplit>& s, uint32_t t, uint64_t w, int ln)
-      : sm(s), tmem(t), wns(w), lane(ln), qd(kmajor(s.q)), pd(kmajor(s.p)), kd(kmajor(s.ring)),
+  __device__ Issuer(Smem<kSplit>& s, uint32_t t, uint64_t w)
+      : sm(s), tmem(t), wns(w), one(elect_one()), qd(kmajor(s.q)), pd(kmajor(s.p)), kd(kmajor(s.ring)),
         // values as the MN-major operand: 64-column slabs 8 KiB apart, 8-token groups 1 KiB apart
         vd(smem_desc(smem_u32(s.ring), kSlab, 1024, kSwizzle128B)) {}
   __device__ void step() {
@@ -373,13 +386,13 @@ struct Issuer {
     }
   }
   __device__ bool scores(int i, bool first, bool last) {
-    if (first && !warp_wait(&sm.q_full, nq++ & 1, 50, wns, lane)) return false;
+    if (first && !warp_wait(&sm.q_full, nq++ & 1, 50, wns)) return false;
     const uint32_t d = tmem + kTmemS + 128 * (i & 1);
 #pragma unroll
     for (int e = 0; e < kSlabs; ++e, step()) {
-      if (!warp_wait(&sm.full[sl], ph, 51, wns, lane)) return false;
+      if (!warp_wait(&sm.full[sl], ph, 51, wns)) return false;
       tc_fence_after();
-      if (lane == 0) {
+      if (one) {
         const uint64_t a = qd + e * (kSlab >> 4), b = kd + (uint32_t)sl * (G::kSlot >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) mma_ss_pair(d, a + 2 * k, b + 2 * k, kIdS, (e | k) ? 1u : 0u);
@@ -400,16 +413,16 @@ struct Issuer {
   }
   // P V of tile i of n items; `first`: it begins its token's output
   __device__ bool values(int i, int n, bool first) {
-    if (!warp_wait(&sm.p_full, i & 1, 52, wns, lane)) return false;
+    if (!warp_wait(&sm.p_full, i & 1, 52, wns)) return false;
     tc_fence_after();
 #pragma unroll
     for (int q = 0; q < kTilePages; ++q) {
       if (q >= n) break;
 #pragma unroll
       for (int j = 0; j < 2; ++j, step()) {
-        if (!warp_wait(&sm.full[sl], ph, 53, wns, lane)) return false;
+        if (!warp_wait(&sm.full[sl], ph, 53, wns)) return false;
         tc_fence_after();
-        if (lane == 0) {
+        if (one) {
           const uint64_t a = pd + q * (kSlab >> 4), b = vd + (uint32_t)sl * (G::kSlot >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -419,15 +432,15 @@ struct Issuer {
         __syncwarp();
       }
     }
-    if (lane == 0) mma_commit_pair(&sm.pv_done, kBoth);
+    if (one) mma_commit_pair(&sm.pv_done, kBoth);
     __syncwarp();
     return true;
   }
 };
 
 template <bool kSplit>
-__device__ void mma_role(Smem<kSplit>& sm, uint32_t tmem, const Params& p, int lane) {
-  Issuer<kSplit> is(sm, tmem, p.wait_ns, lane);
+__device__ void mma_role(Smem<kSplit>& sm, uint32_t tmem, const Params& p) {
+  Issuer<kSplit> is(sm, tmem, p.wait_ns);
   int i = 0, n_prev = 0;
   bool ok = true, first_prev = false;
   for (Walk w(p.q, sm.from, sm.to); ok && w.valid(); w.next()) {
@@ -440,8 +453,8 @@ __device__ void mma_role(Smem<kSplit>& sm, uint32_t tmem, const Params& p, int l
   }
   if (ok && i > 0) ok = is.values(i - 1, n_prev, first_prev);
   if (!ok) set_abort(sm);
-  if (lane == 0) mma_commit_pair(&sm.fin, 1);
-  warp_wait(&sm.fin, 0, 54, p.wait_ns, lane);
+  if (is.one) mma_commit_pair(&sm.fin, 1);
+  warp_wait(&sm.fin, 0, 54, p.wait_ns);
 }
 
 // ---------------------------------------------------------------- softmax and output
@@ -460,11 +473,11 @@ struct Softmax {
     xl[ch][l] = lsum;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.lbar);
-    if (!warp_wait(&sm.lbar, n_out & 1, 60, p.wait_ns, lane)) return false;
+    if (!warp_wait(&sm.lbar, n_out & 1, 60, p.wait_ns)) return false;
     // the same order of additions in all four threads of the head
     const int l0 = l & 63;
     const float tot = (xl[0][l0] + xl[1][l0]) + (xl[0][l0 + 64] + xl[1][l0 + 64]);
-    if (!warp_wait(&sm.pv_done, last_tile & 1, 61, p.wait_ns, lane)) return false;
+    if (!warp_wait(&sm.pv_done, last_tile & 1, 61, p.wait_ns)) return false;
     tc_fence_after();
     ++n_out;
     const float inv = tot == 0.f ? 0.f : 1.f / tot;  // no visible row: zero (a NaN sum stays NaN)
@@ -532,7 +545,7 @@ struct Softmax {
             report(MLA_ERR_BOUNDS, 22, w.at.b, phys);
           }
         }
-        if (!warp_wait(&sm.s_full[i & 1], (i >> 1) & 1, 62, p.wait_ns, lane)) return false;
+        if (!warp_wait(&sm.s_full[i & 1], (i >> 1) & 1, 62, p.wait_ns)) return false;
         tc_fence_after();
         float s[64];
         {
@@ -557,7 +570,7 @@ struct Softmax {
         sm.xm[i & 1][ch][l] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.xbar[i & 1]);
-        if (!warp_wait(&sm.xbar[i & 1], (i >> 1) & 1, 63, p.wait_ns, lane)) return false;
+        if (!warp_wait(&sm.xbar[i & 1], (i >> 1) & 1, 63, p.wait_ns)) return false;
         const float m_tile = fmaxf(fmaxf(sm.xm[i & 1][0][l], sm.xm[i & 1][1][l]),
                                    fmaxf(sm.xm[i & 1][0][l ^ 64], sm.xm[i & 1][1][l ^ 64]));
         const bool first = t == 0;
@@ -589,7 +602,7 @@ struct Softmax {
         if (first && open) {
           if (!finish(l_prev, m_prev, open_tok, open_whole, open_slot, i - 1)) return false;
         } else if (i >= 1) {
-          if (!warp_wait(&sm.pv_done, (i - 1) & 1, 64, p.wait_ns, lane)) return false;
+          if (!warp_wait(&sm.pv_done, (i - 1) & 1, 64, p.wait_ns)) return false;
           tc_fence_after();
         }
         if (!first && __any_sync(0xffffffffu, rescale)) {
@@ -685,9 +698,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        kHalfH * rank + (l & 63), worker};
     if (!so.run(from, to)) set_abort(sm);
   } else if (warp == kMmaWarp) {
-    if (rank == 0) mma_role(sm, tmem, p, lane);
+    if (rank == 0) mma_role(sm, tmem, p);
   } else if (warp == kQueryWarp) {
-    query_role(sm, &qmap, p, rank, lane);
+    query_role(sm, &qmap, p, rank);
   } else {
     load_role<kSplit, Maps>(sm, pool, &qlomap, p, warp - kLoadWarp0, rank, lane);
   }
