@@ -68,8 +68,8 @@ constexpr int kSlabs = kRow / 64;
 constexpr int kSlab = 64 * 128;  // 64 rows x 64 bf16, 128-byte swizzle
 constexpr int kKvSlot = 2 * kSlab;
 constexpr int kTmemS = 0, kTmemO = 256, kTmemCols = 512;
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp0 = 9, kLoadWarps = 4, kQueryWarp = 13;
-constexpr int kThreads = 32 * 14;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp0 = 9, kLoadWarps = 2, kQueryWarp = 11;
+constexpr int kThreads = 32 * 12;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint16_t kBoth = 3;
 constexpr int kMaxWorkers = 1024;
@@ -83,6 +83,18 @@ struct Geo {
   static constexpr int kSlots = kSplit ? 4 : 7;
 };
 
+// A tile as the MMA and softmax warps need it, handed to them by the first load
+// warp of their CTA: 4 records in turn, and one with n = 0 behind the last.  The
+// ring keeps that warp within a tile of the MMAs, so a record is read by all
+// before the one four tiles on replaces it.
+struct Tile {
+  int n;                   // items
+  int first, last, whole;  // the tile begins / ends its piece; the piece is the whole token
+  int tok, slot;           // the piece's token, its place in the workspace
+  int lo[kTilePages], hi[kTilePages];  // per item: visible columns of its 64, as the loads shift them
+};
+constexpr int kTiles = 4;
+
 template <bool kSplit>
 struct Smem {
   using G = Geo<kSplit>;
@@ -90,7 +102,8 @@ struct Smem {
   uint8_t p[kTilePages][kSlab];              // P of the tile: per item 64 heads x 64 tokens
   uint8_t ring[G::kSlots][G::kSlot];         // the prefix sums of the cut, then the ring
   uint64_t full[G::kSlots], empty[G::kSlots];
-  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, fin, xbar[2], lbar;
+  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, fin, xbar[2], lbar, tile_full[kTiles];
+  Tile tile[kTiles];
   float xm[2][2][128];                       // [tile parity][column half] maximum of each lane's columns
   float xl[2][2][128];                       // [piece parity][column half] partial row sums of a finished piece
   long long warp_sum[kThreads / 32];
@@ -221,43 +234,56 @@ __device__ void find_range(Smem<kSplit>& sm, const Params& p, int worker) {
 }
 
 // ---------------------------------------------------------------- TMA producers
-// The four items of a tile as the loads need them.
-struct TileLoad {
-  int n;                        // items
-  int phys[kTilePages], y[kTilePages], m[kTilePages];  // page, first row of the box, tensor map
+// The tiles of a range in order.
+struct Cursor {
+  Walk w;
+  int tile, n;  // tile of the piece; items of the tile
+  __device__ Cursor(const Batch& q, Place from, Place to) : w(q, from, to), tile(0) { settle(); }
+  __device__ void settle() {
+    while (w.valid() && w.tiles() == 0) w.next();
+    n = w.valid() ? min(kTilePages, w.k1 - w.at.k - tile * kTilePages) : 0;
+  }
+  __device__ bool valid() const { return n > 0; }
+  __device__ void next() {
+    if (++tile == w.tiles()) {
+      tile = 0;
+      w.next();
+    }
+    settle();
+  }
 };
 
+// An item as the loads need it, held by lane i for item i of a tile.
+struct ItemLoad {
+  int phys, y, m;  // page, first row of the box, tensor map
+  int lo, hi;      // columns of the scores that are visible
+};
+
+// The table lookup of lane i's item; nothing waits for it before it is used.
 template <typename Maps>
-__device__ __forceinline__ TileLoad tile_load(const Params& p, const Walk& w, int tile, int lane) {
-  TileLoad t;
-  const int k0 = w.at.k + tile * kTilePages;
-  t.n = min(kTilePages, w.k1 - k0);
-  // lanes 0..3 look up one item each
-  int phys = 0, y = 0, m = 0;
-  if (lane < t.n) {
-    const Item it = item_of(p.q.vis, w.position(), k0 + lane);
-    phys = p.block_table[(long long)w.at.b * p.max_blocks + it.page];
-    if (phys < 0 || phys >= p.num_blocks) phys = p.num_blocks;  // outside the pool: arrives as zeros (masked too)
-    if (it.b == kPage) {
-      y = it.a;
-      m = sizeof(Maps) / sizeof(CUtensorMap) - 1;
-    } else if (it.a == 0 || sizeof(Maps) == sizeof(CUtensorMap)) {
-      y = it.b - kPage;  // rows past the range fall behind the page's top, negative rows arrive as zeros
-      m = sizeof(Maps) / sizeof(CUtensorMap) - 1;
+__device__ __forceinline__ ItemLoad item_load(const Params& p, const Cursor& c, int lane) {
+  constexpr int kWhole = sizeof(Maps) / sizeof(CUtensorMap) - 1;
+  ItemLoad t{p.num_blocks, 0, kWhole, 0, 0};
+  if (lane < c.n) {
+    const Item it = item_of(p.q.vis, c.w.position(), c.w.at.k + c.tile * kTilePages + lane);
+    t.phys = p.block_table[(long long)c.w.at.b * p.max_blocks + it.page];
+    t.lo = 0;
+    t.hi = it.b - it.a;
+    if (it.a == 0) {  // rows past the range fall behind the page's top, negative rows arrive as zeros
+      t.y = it.b - kPage;
+      t.lo = kPage - it.b;
+      t.hi = kPage;
     } else {
-      y = it.a;
-      m = it.b - 1;
+      t.y = it.a;
+      if (it.b < kPage) t.m = it.b - 1;  // only with a map for every end, see chunk_tc_impl
     }
-  }
-#pragma unroll
-  for (int i = 0; i < kTilePages; ++i) {
-    t.phys[i] = __shfl_sync(0xffffffffu, phys, i);
-    t.y[i] = __shfl_sync(0xffffffffu, y, i);
-    t.m[i] = __shfl_sync(0xffffffffu, m, i);
   }
   return t;
 }
 
+// Both CTAs' load warps arrive on every slot, also where a CTA has nothing to
+// load (a tile of one or two items): the MMAs never run more than a ring ahead
+// of either, so a phase of `empty` is always seen before the next one ends.
 template <bool kSplit, typename Maps>
 struct Loader {
   using G = Geo<kSplit>;
@@ -280,32 +306,34 @@ struct Loader {
   __device__ bool ready() {
     return use == 0 || warp_wait(&sm.empty[sl], (use - 1) & 1, 40, p.wait_ns);
   }
-  // the 9 key slabs of a tile of token `tok`
-  __device__ bool keys(const TileLoad& t, int tok) {
+  // the 9 key slabs of a tile of n items of token `tok`
+  __device__ bool keys(const ItemLoad& it, int n, int tok) {
+    const int phys[2] = {__shfl_sync(0xffffffffu, it.phys, 2 * rank), __shfl_sync(0xffffffffu, it.phys, 2 * rank + 1)};
+    const int y[2] = {__shfl_sync(0xffffffffu, it.y, 2 * rank), __shfl_sync(0xffffffffu, it.y, 2 * rank + 1)};
+    const int m[2] = {__shfl_sync(0xffffffffu, it.m, 2 * rank), __shfl_sync(0xffffffffu, it.m, 2 * rank + 1)};
 #pragma unroll 1
     for (int e = 0; e < kSlabs; ++e, step()) {
       if (!mine()) continue;
       if (!ready()) return false;
       if (one) {
         const uint32_t bar = leader(&sm.full[sl]);
-        if (rank == 0) mbar_arrive_expect_tx(&sm.full[sl], t.n * kSlab + (kSplit ? 2 * kSlab : 0));
+        if (rank == 0) mbar_arrive_expect_tx(&sm.full[sl], n * kSlab + (kSplit ? 2 * kSlab : 0));
+        else mbar_arrive_remote(bar);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = 2 * rank + h;
-          const int phys = rank ? t.phys[2 + h] : t.phys[h], y = rank ? t.y[2 + h] : t.y[h], m = rank ? t.m[2 + h] : t.m[h];
-          if (i < t.n) tma_load_3d_pair(sm.ring[sl] + h * kSlab, &pool.end[m], 64 * e, y, phys, bar);
-        }
+        for (int h = 0; h < 2; ++h)
+          if (2 * rank + h < n) tma_load_3d_pair(sm.ring[sl] + h * kSlab, &pool.end[m[h]], 64 * e, y[h], phys[h], bar);
         if (kSplit) tma_load_2d_pair(sm.ring[sl] + kKvSlot, qlo, 64 * e, tok * kH + kHalfH * rank, bar);
       }
       __syncwarp();
     }
     return true;
   }
-  // the value columns of a tile: per item two blocks of 256 columns
-  __device__ bool values(const TileLoad& t) {
-#pragma unroll
-    for (int i = 0; i < kTilePages; ++i) {
-      if (i >= t.n) break;
+  // the value columns of a tile of n items: per item two blocks of 256 columns
+  __device__ bool values(const ItemLoad& it, int n) {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int phys = __shfl_sync(0xffffffffu, it.phys, i), y = __shfl_sync(0xffffffffu, it.y, i),
+                m = __shfl_sync(0xffffffffu, it.m, i);
 #pragma unroll 1
       for (int j = 0; j < 2; ++j, step()) {
         if (!mine()) continue;
@@ -313,10 +341,10 @@ struct Loader {
         if (one) {
           const uint32_t bar = leader(&sm.full[sl]);
           if (rank == 0) mbar_arrive_expect_tx(&sm.full[sl], 2 * kKvSlot);
+          else mbar_arrive_remote(bar);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            tma_load_3d_pair(sm.ring[sl] + h * kSlab, &pool.end[t.m[i]], 256 * j + 128 * rank + 64 * h, t.y[i], t.phys[i],
-                             bar);
+            tma_load_3d_pair(sm.ring[sl] + h * kSlab, &pool.end[m], 256 * j + 128 * rank + 64 * h, y, phys, bar);
         }
         __syncwarp();
       }
@@ -327,29 +355,85 @@ struct Loader {
 
 template <bool kSplit, typename Maps>
 __device__ void load_role(Smem<kSplit>& sm, const Maps& pool, const CUtensorMap* qlo, const Params& p, int me, int rank,
-                          int lane) {
+                          int worker, int lane) {
   Loader<kSplit, Maps> ld{sm, pool, qlo, p, me, rank, elect_one()};
-  TileLoad prev;
-  prev.n = 0;
+  Cursor c(p.q, sm.from, sm.to);
+  ItemLoad next = item_load<Maps>(p, c, lane), prev{};
+  int n_prev = 0, i = 0;
   bool ok = true;
-  for (Walk w(p.q, sm.from, sm.to); ok && w.valid(); w.next()) {
-    const int nt = w.tiles(), tok = w.token();
-    for (int i = 0; ok && i < nt; ++i) {
-      const TileLoad t = tile_load<Maps>(p, w, i, lane);
-      ok = ld.keys(t, tok) && ld.values(prev) && !aborted(sm);
-      prev = t;
+  while (ok && c.valid()) {
+    ItemLoad it = next;
+    const int n = c.n, tok = c.w.token(), b = c.w.at.b;
+    Tile t;
+    t.n = n;
+    t.first = c.tile == 0;
+    t.last = c.tile + 1 == c.w.tiles();
+    t.whole = c.w.whole();
+    t.tok = tok;
+    t.slot = 2 * worker + (c.w.at.k > 0 ? 0 : 1);
+    c.next();
+    next = item_load<Maps>(p, c, lane);
+    if (lane < n && (it.phys < 0 || it.phys >= p.num_blocks)) {
+      if (me == 0 && rank == 0) report(MLA_ERR_BOUNDS, 22, b, it.phys);
+      it.phys = p.num_blocks;  // outside the pool: arrives as zeros, and is not visible
+      it.lo = it.hi = 0;
     }
+    if (me == 0) {
+      Tile& d = sm.tile[i % kTiles];
+      if (lane < kTilePages) {
+        d.lo[lane] = it.lo;
+        d.hi[lane] = it.hi;
+      }
+      if (lane == 0) {
+        d.n = t.n;
+        d.first = t.first;
+        d.last = t.last;
+        d.whole = t.whole;
+        d.tok = t.tok;
+        d.slot = t.slot;
+      }
+      __syncwarp();
+      if (ld.one) mbar_arrive(&sm.tile_full[i % kTiles]);
+      __syncwarp();
+    }
+    ok = ld.keys(it, n, tok) && ld.values(prev, n_prev) && !aborted(sm);
+    prev = it;
+    n_prev = n;
+    ++i;
   }
-  if (ok) ok = ld.values(prev);
+  if (me == 0) {
+    if (lane == 0) sm.tile[i % kTiles].n = 0;
+    __syncwarp();
+    if (ld.one) mbar_arrive(&sm.tile_full[i % kTiles]);
+    __syncwarp();
+  }
+  if (ok) ok = ld.values(prev, n_prev);
   if (!ok) set_abort(sm);
 }
 
+// Record i: false if the wait ran out.
 template <bool kSplit>
-__device__ void query_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, int rank) {
+__device__ __forceinline__ bool wait_tile(Smem<kSplit>& sm, int i, uint64_t wns) {
+  return warp_wait(&sm.tile_full[i % kTiles], (i / kTiles) & 1, 42, wns);
+}
+
+// The queries of the pieces, one at a time; and, as no other warp meets them,
+// the rows of tokens that see nothing: zeros, log-sum-exp of an empty set.
+template <bool kSplit>
+__device__ void query_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, int rank, int lane) {
   const bool one = elect_one();
   int n = 0;
   for (Walk w(p.q, sm.from, sm.to); w.valid(); w.next()) {
-    if (w.tiles() == 0) continue;
+    const int tok = w.token();
+    if (w.tiles() == 0) {
+      const long long row = (long long)tok * kH + kHalfH * rank;
+      uint4* dst = reinterpret_cast<uint4*>(p.o_lat + row * kDc);
+      for (int i = lane; i < kHalfH * kDc / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+      if (p.lse != nullptr)
+        for (int h = lane; h < kHalfH; h += 32) p.lse[row + h] = -INFINITY;
+      __syncwarp();
+      continue;
+    }
     if (n >= 1 && !warp_wait(&sm.q_empty, (n - 1) & 1, 41, p.wait_ns)) {
       set_abort(sm);
       return;
@@ -357,7 +441,7 @@ __device__ void query_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Para
     if (one) {
       if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kSlabs * kSlab);
       for (int e = 0; e < kSlabs; ++e)
-        tma_load_2d_pair(sm.q[e], qmap, 64 * e, w.token() * kH + kHalfH * rank, leader(&sm.q_full));
+        tma_load_2d_pair(sm.q[e], qmap, 64 * e, tok * kH + kHalfH * rank, leader(&sm.q_full));
     }
     __syncwarp();
     ++n;
@@ -443,13 +527,16 @@ __device__ void mma_role(Smem<kSplit>& sm, uint32_t tmem, const Params& p) {
   Issuer<kSplit> is(sm, tmem, p.wait_ns);
   int i = 0, n_prev = 0;
   bool ok = true, first_prev = false;
-  for (Walk w(p.q, sm.from, sm.to); ok && w.valid(); w.next()) {
-    const int nt = w.tiles(), n = w.k1 - w.at.k;
-    for (int t = 0; ok && t < nt; ++t, ++i) {
-      ok = is.scores(i, t == 0, t == nt - 1) && (i == 0 || is.values(i - 1, n_prev, first_prev)) && !aborted(sm);
-      n_prev = min(kTilePages, n - t * kTilePages);
-      first_prev = t == 0;
-    }
+  for (;; ++i) {
+    ok = ok && wait_tile(sm, i, p.wait_ns);
+    if (!ok) break;
+    const Tile& t = sm.tile[i % kTiles];
+    const int n = uni(t.n);
+    const bool first = uni(t.first), last = uni(t.last);
+    if (n == 0) break;
+    ok = is.scores(i, first, last) && (i == 0 || is.values(i - 1, n_prev, first_prev));
+    n_prev = n;
+    first_prev = first;
   }
   if (ok && i > 0) ok = is.values(i - 1, n_prev, first_prev);
   if (!ok) set_abort(sm);
@@ -458,183 +545,245 @@ __device__ void mma_role(Smem<kSplit>& sm, uint32_t tmem, const Params& p) {
 }
 
 // ---------------------------------------------------------------- softmax and output
+// Two floats in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <bool kSplit>
 struct Softmax {
   Smem<kSplit>& sm;
   const Params& p;
   const uint32_t tl;               // this warp's TMEM lane quarter
   const int lane, l, half, ch, head;
-  int worker;
   int n_out = 0;                   // pieces written (parity of lbar)
 
-  // The finished piece's output: row sums of the head's four threads, then O / l.
-  __device__ bool finish(float lsum, float m, int tok, bool whole, int slot, int last_tile) {
+  // A finished piece: its row sum (this thread's share), its maximum (in units
+  // of the raw scores) and where it goes.
+  struct Piece {
+    float lsum, m;
+    int tok, slot, whole;
+  };
+
+  // The piece's factor 1 / l and log2-sum-exp, from the shares of the head's four threads.
+  __device__ bool total(const Piece& d, float& inv) {
     float(&xl)[2][128] = sm.xl[n_out & 1];
-    xl[ch][l] = lsum;
+    xl[ch][l] = d.lsum;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.lbar);
     if (!warp_wait(&sm.lbar, n_out & 1, 60, p.wait_ns)) return false;
+    ++n_out;
     // the same order of additions in all four threads of the head
     const int l0 = l & 63;
     const float tot = (xl[0][l0] + xl[1][l0]) + (xl[0][l0 + 64] + xl[1][l0 + 64]);
-    if (!warp_wait(&sm.pv_done, last_tile & 1, 61, p.wait_ns)) return false;
-    tc_fence_after();
-    ++n_out;
-    const float inv = tot == 0.f ? 0.f : 1.f / tot;  // no visible row: zero (a NaN sum stays NaN)
-    const float lse = tot == 0.f ? -INFINITY : m + log2f(tot);
-    const int col = 256 * ch + 128 * half;  // this thread's 128 latent columns
+    inv = tot == 0.f ? 0.f : 1.f / tot;  // no visible row: zero (a NaN sum stays NaN)
     if (half == 0 && ch == 0) {
-      if (!whole) p.part_lse[(long long)slot * kH + head] = lse;
-      else if (p.lse != nullptr) p.lse[(long long)tok * kH + head] = lse;
+      const float lse = tot == 0.f ? -INFINITY : fmaf(d.m, p.scale_log2, log2f(tot));
+      if (!d.whole) p.part_lse[(long long)d.slot * kH + head] = lse;
+      else if (p.lse != nullptr) p.lse[(long long)d.tok * kH + head] = lse;
     }
-    bf16* out = p.o_lat + ((long long)tok * kH + head) * kDc + col;
-    float* part = p.part_o + ((long long)slot * kH + head) * kDc + col;
+    return true;
+  }
+
+  // This thread's 128 output columns [256 ch + 128 half, + 128) of its head.
+  // A whole token's are read out and rounded to registers first (the next
+  // tile's P V may then begin) and written by store_whole; a part's go to the
+  // workspace at once.
+  __device__ void read_whole(float inv, uint32_t (&out)[64]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      tmem_ld32(tl + kTmemO + 128 * ch + 32 * c, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        out[16 * c + k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+    }
+  }
+  __device__ void store_whole(int tok, const uint32_t (&out)[64]) {
+    uint4* dst = reinterpret_cast<uint4*>(p.o_lat + ((long long)tok * kH + head) * kDc + 256 * ch + 128 * half);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) dst[k] = make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
+  }
+  __device__ void write_part(int slot, float inv) {
+    float* part = p.part_o + ((long long)slot * kH + head) * kDc + 256 * ch + 128 * half;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[32];
       tmem_ld32(tl + kTmemO + 128 * ch + 32 * c, o);
       tmem_wait_ld();
       const float* f = reinterpret_cast<const float*>(o);
-      if (whole) {
-        uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
+      float4* dst = reinterpret_cast<float4*>(part + 32 * c);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          dst[k] = make_uint4(pack_bf16x2(f[8 * k] * inv, f[8 * k + 1] * inv), pack_bf16x2(f[8 * k + 2] * inv, f[8 * k + 3] * inv),
-                              pack_bf16x2(f[8 * k + 4] * inv, f[8 * k + 5] * inv), pack_bf16x2(f[8 * k + 6] * inv, f[8 * k + 7] * inv));
-      } else {
-        float4* dst = reinterpret_cast<float4*>(part + 32 * c);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          dst[k] = make_float4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
-      }
+      for (int k = 0; k < 8; ++k)
+        dst[k] = make_float4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
     }
+  }
+
+  __device__ void arrive_p() {
+    fence_proxy_async_smem();
     tc_fence_before();
-    return true;
+    __syncwarp();
+    if (lane == 0) mbar_arrive_remote(leader(&sm.p_full));
   }
 
-  // A token that sees nothing: zeros, log-sum-exp of an empty set.
-  __device__ void write_empty(int tok) {
-    uint4* dst = reinterpret_cast<uint4*>(p.o_lat + ((long long)tok * kH + head) * kDc + 256 * ch + 128 * half);
-#pragma unroll 1
-    for (int k = 0; k < 16; ++k) dst[k] = make_uint4(0, 0, 0, 0);
-    if (half == 0 && ch == 0 && p.lse != nullptr) p.lse[(long long)tok * kH + head] = -INFINITY;
-  }
-
-  __device__ bool run(const Place& from, const Place& to) {
+  __device__ bool run() {
     float m_used = -INFINITY, lsum = 0.f;
-    // the piece whose output is still in TMEM
-    bool open = false, open_whole = false;
-    int open_tok = 0, open_slot = 0, i = 0;
-    for (Walk w(p.q, from, to); w.valid(); w.next()) {
-      const int nt = w.tiles();
-      if (nt == 0) {
-        write_empty(w.token());
-        continue;
-      }
-      for (int t = 0; t < nt; ++t, ++i) {
-        // this thread's item: which of the tile's rows are visible
-        const int k = w.at.k + t * kTilePages + 2 * half + ch;
-        int lo = kPage, hi = kPage;
-        if (k < w.k1) {
-          const Item it = item_of(p.q.vis, w.position(), k);
-          const int phys = p.block_table[(long long)w.at.b * p.max_blocks + it.page];
-          if (phys >= 0 && phys < p.num_blocks) {
-            lo = it.a == 0 ? kPage - it.b : 0;  // as the loads shift them
-            hi = it.a == 0 ? kPage : it.b - it.a;
-          } else if (lane == 0) {
-            report(MLA_ERR_BOUNDS, 22, w.at.b, phys);
-          }
-        }
-        if (!warp_wait(&sm.s_full[i & 1], (i >> 1) & 1, 62, p.wait_ns)) return false;
-        tc_fence_after();
-        float s[64];
-        {
-          uint32_t a[32], b[32];
-          const uint32_t at = tl + kTmemS + 128 * (i & 1) + 64 * ch;
-          tmem_ld32(at, a);
-          tmem_ld32(at + 32, b);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            s[c] = __uint_as_float(a[c]);
-            s[32 + c] = __uint_as_float(b[c]);
-          }
-        }
-        tc_fence_before();
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          s[c] = c >= lo && c < hi ? s[c] * p.scale_log2 : -INFINITY;
-          mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-        }
-        sm.xm[i & 1][ch][l] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.xbar[i & 1]);
-        if (!warp_wait(&sm.xbar[i & 1], (i >> 1) & 1, 63, p.wait_ns)) return false;
-        const float m_tile = fmaxf(fmaxf(sm.xm[i & 1][0][l], sm.xm[i & 1][1][l]),
-                                   fmaxf(sm.xm[i & 1][0][l ^ 64], sm.xm[i & 1][1][l ^ 64]));
-        const bool first = t == 0;
-        const float m_prev = m_used, l_prev = lsum;  // of the open piece, when this tile begins another
-        if (first) {
-          m_used = -INFINITY;
-          lsum = 0.f;
-        }
-        // rescale only when P could grow past 2^8: P and O are exact in the scale
-        float alpha = 1.f;
-        const bool rescale = m_tile > m_used + kRescaleLog2;
-        if (rescale) {
-          alpha = exp2_fast(m_used - m_tile);  // 0 at the piece's first finite maximum
-          m_used = m_tile;
-        }
-        const float base = m_used == -INFINITY ? 0.f : m_used;
-        uint32_t pk[32];
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+    Piece open{0.f, 0.f, 0, 0, 0};
+    uint32_t out[64];
+    int i = 0;
+    const int q = 2 * half + ch;  // this warp's item of every tile
+    uint8_t* row = sm.p[q] + (l & 63) * 128;
+    for (;; ++i) {
+      if (!wait_tile(sm, i, p.wait_ns)) return false;
+      const Tile& t = sm.tile[i % kTiles];
+      const int n = uni(t.n);
+      if (n == 0) break;
+      const bool first = uni(t.first);
+      const int lo = uni(t.lo[q]), hi = uni(t.hi[q]);
+      const int tok = t.tok, slot = t.slot, whole = t.whole;
+      if (!warp_wait(&sm.s_full[i & 1], (i >> 1) & 1, 62, p.wait_ns)) return false;
+      tc_fence_after();
+      float s[64];
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (hi > lo) {
+        uint32_t a[32], b[32];
+        const uint32_t at = tl + kTmemS + 128 * (i & 1) + 64 * ch;
+        tmem_ld32(at, a);
+        tmem_ld32(at + 32, b);
+        tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          const float p0 = exp2_fast(s[2 * c] - base), p1 = exp2_fast(s[2 * c + 1] - base);
-          ps[c & 3] += p0 + p1;
-          pk[c] = pack_bf16x2(p0, p1);
+          s[c] = __uint_as_float(a[c]);
+          s[32 + c] = __uint_as_float(b[c]);
         }
-        lsum = lsum * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-
-        // P V of the tile before reads P and adds to O: it must be over before
-        // this tile writes P, rescales O or hands O to the next token.
-        if (first && open) {
-          if (!finish(l_prev, m_prev, open_tok, open_whole, open_slot, i - 1)) return false;
-        } else if (i >= 1) {
-          if (!warp_wait(&sm.pv_done, (i - 1) & 1, 64, p.wait_ns)) return false;
-          tc_fence_after();
-        }
-        if (!first && __any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            const uint32_t a = tl + kTmemO + 128 * ch + 32 * c;
-            tmem_ld32(a, o);
-            tmem_wait_ld();
+        if (hi - lo < kPage) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(a, o);
-          }
-          tmem_wait_st();
+          for (int c = 0; c < 64; ++c)
+            if (c < lo || c >= hi) s[c] = -INFINITY;
         }
-        // row hl of the item's P slab, K-major with the 128-byte swizzle
-        const int hl = l & 63;
-        uint8_t* row = sm.p[2 * half + ch] + hl * 128;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+      }
+      tc_fence_before();
+      sm.xm[i & 1][ch][l] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.xbar[i & 1]);
+      if (!warp_wait(&sm.xbar[i & 1], (i >> 1) & 1, 63, p.wait_ns)) return false;
+      const float m_tile = fmaxf(fmaxf(sm.xm[i & 1][0][l], sm.xm[i & 1][1][l]),
+                                 fmaxf(sm.xm[i & 1][0][l ^ 64], sm.xm[i & 1][1][l ^ 64]));
+      const bool close = first && i > 0;  // another piece's output is still in TMEM
+      if (first) {
+        open.lsum = lsum;
+        open.m = m_used;
+        m_used = -INFINITY;
+        lsum = 0.f;
+      }
+      // rescale only when P could grow past 2^8: P and O are exact in the scale
+      float alpha = 1.f;
+      const bool rescale = (m_tile - m_used) * p.scale_log2 > kRescaleLog2;  // never from -inf to -inf (NaN)
+      if (rescale) {
+        alpha = exp2_fast((m_used - m_tile) * p.scale_log2);  // 0 at the piece's first finite maximum
+        m_used = m_tile;
+      }
+      const float base = m_used == -INFINITY ? 0.f : -m_used * p.scale_log2;
+      uint32_t pk[32];
+      if (hi > lo) {
+        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(base, base);
+        uint64_t sum2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float x, y;
+          unpack2(fma2(pack2(s[2 * c], s[2 * c + 1]), scale2, base2), x, y);
+          x = exp2_fast(x);
+          y = exp2_fast(y);
+          sum2[c & 1] = add2(sum2[c & 1], pack2(x, y));
+          pk[c] = pack_bf16x2(x, y);
+        }
+        float x, y;
+        unpack2(add2(sum2[0], sum2[1]), x, y);
+        lsum = fmaf(lsum, alpha, x + y);
+      } else {
+        lsum *= alpha;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] = 0;
+      }
+
+      // P V of the tile before reads P and adds to O: it must be over before
+      // this tile writes P, rescales O or hands O to the next piece.
+      if (i >= 1) {
+        if (!warp_wait(&sm.pv_done, (i - 1) & 1, 64, p.wait_ns)) return false;
+        tc_fence_after();
+      }
+      if (!first && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          const uint32_t a = tl + kTmemO + 128 * ch + 32 * c;
+          tmem_ld32(a, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(a, o);
+        }
+        tmem_wait_st();
+      }
+      // row hl of the item's P slab, K-major with the 128-byte swizzle
+      if (q < n) {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(row + ((c ^ (hl & 7)) << 4)) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(leader(&sm.p_full));
+          *reinterpret_cast<uint4*>(row + ((c ^ (l & 7)) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       }
-      open = true;
-      open_whole = w.whole();
-      open_tok = w.token();
-      open_slot = 2 * worker + (w.at.k > 0 ? 0 : 1);
+      if (close) {
+        float inv;
+        if (!total(open, inv)) return false;
+        if (open.whole) {
+          read_whole(inv, out);
+          arrive_p();
+          store_whole(open.tok, out);
+        } else {
+          write_part(open.slot, inv);
+          arrive_p();
+        }
+      } else {
+        arrive_p();
+      }
+      if (first) {
+        open.tok = tok;
+        open.slot = slot;
+        open.whole = whole;
+      }
     }
-    return !open || finish(lsum, m_used, open_tok, open_whole, open_slot, i - 1);
+    if (i > 0) {
+      open.lsum = lsum;
+      open.m = m_used;
+      float inv;
+      if (!warp_wait(&sm.pv_done, (i - 1) & 1, 65, p.wait_ns) || !total(open, inv)) return false;
+      tc_fence_after();
+      if (open.whole) {
+        read_whole(inv, out);
+        store_whole(open.tok, out);
+      } else {
+        write_part(open.slot, inv);
+      }
+    }
+    return true;
   }
 };
 
@@ -652,7 +801,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < G::kSlots; ++s) {
-      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.full[s], 2);
       mbar_init(&sm.empty[s], 1);
     }
     mbar_init(&sm.q_full, 1);
@@ -664,6 +813,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&sm.p_full, 2 * kSoftmaxWarps);
     mbar_init(&sm.pv_done, 1);
     mbar_init(&sm.lbar, kSoftmaxWarps);
+    for (int b = 0; b < kTiles; ++b) mbar_init(&sm.tile_full[b], 1);
     mbar_init(&sm.fin, 1);
     sm.abort_flag = 0;
     fence_mbar_init();
@@ -695,14 +845,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp < kSoftmaxWarps) {
     const int l = (warp & 3) * 32 + lane;
     Softmax<kSplit> so{sm, p, tmem + ((uint32_t)((warp & 3) * 32) << 16), lane, l, l >> 6, warp >> 2,
-                       kHalfH * rank + (l & 63), worker};
-    if (!so.run(from, to)) set_abort(sm);
+                       kHalfH * rank + (l & 63)};
+    if (!so.run()) set_abort(sm);
   } else if (warp == kMmaWarp) {
     if (rank == 0) mma_role(sm, tmem, p);
   } else if (warp == kQueryWarp) {
-    query_role(sm, &qmap, p, rank);
+    query_role(sm, &qmap, p, rank, lane);
   } else {
-    load_role<kSplit, Maps>(sm, pool, &qlomap, p, warp - kLoadWarp0, rank, lane);
+    load_role<kSplit, Maps>(sm, pool, &qlomap, p, warp - kLoadWarp0, rank, worker, lane);
   }
 
   tc_fence_before();
