@@ -37,8 +37,9 @@
 // columns and lanes 64..127 the second.  So the softmax thread of lane l and
 // column half ch owns one item of the tile, q = 2 (l / 64) + ch.
 //
-// Warp roles (448 threads): warps 0..7 softmax and output, warp 8 issues the
-// MMAs (leader CTA), warps 9..12 load the ring, warp 13 the queries.
+// Warp roles (384 threads): warps 0..7 softmax and output, warp 8 issues the
+// MMAs (leader CTA), warps 9 and 10 load the ring, warp 11 plans the tiles and
+// loads the queries.
 //
 // Rows that are not visible never reach an MMA: a page's box is shifted so
 // that they fall outside the page and arrive as zeros, or, when the range is
@@ -83,15 +84,14 @@ struct Geo {
   static constexpr int kSlots = kSplit ? 4 : 7;
 };
 
-// A tile as the MMA and softmax warps need it, handed to them by the first load
-// warp of their CTA: 4 records in turn, and one with n = 0 behind the last.  The
-// ring keeps that warp within a tile of the MMAs, so a record is read by all
-// before the one four tiles on replaces it.
+// A tile as the load, MMA and softmax warps of a CTA need it, planned by its
+// query warp up to kTiles ahead; one with n = 0 comes behind the last.
 struct Tile {
   int n;                   // items
   int first, last, whole;  // the tile begins / ends its piece; the piece is the whole token
   int tok, slot;           // the piece's token, its place in the workspace
-  int lo[kTilePages], hi[kTilePages];  // per item: visible columns of its 64, as the loads shift them
+  int phys[kTilePages], y[kTilePages], map[kTilePages];  // per item: page, first row of the box, tensor map
+  int lo[kTilePages], hi[kTilePages];                    // visible columns of its 64 scores, as the box shifts them
 };
 constexpr int kTiles = 4;
 
@@ -102,10 +102,10 @@ struct Smem {
   uint8_t p[kTilePages][kSlab];              // P of the tile: per item 64 heads x 64 tokens
   uint8_t ring[G::kSlots][G::kSlot];         // the prefix sums of the cut, then the ring
   uint64_t full[G::kSlots], empty[G::kSlots];
-  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, fin, xbar[2], lbar, tile_full[kTiles];
+  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, fin, xbar[2], lbar, tile_full[kTiles], tile_empty[kTiles];
   Tile tile[kTiles];
   float xm[2][2][128];                       // [tile parity][column half] maximum of each lane's columns
-  float xl[2][2][128];                       // [piece parity][column half] partial row sums of a finished piece
+  float xl[2][2][128];                       // [tile parity][column half] shares of a finished piece's row sums
   long long warp_sum[kThreads / 32];
   Place from, to;                            // this worker's range
   uint32_t tmem_base;
@@ -181,6 +181,14 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// 2-D tile store of a shared-memory box, tracked by this thread's bulk groups.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // All lanes of a converged warp wait; the outcome is the warp's.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int where, uint64_t wns) {
   const bool ok = mbar_try_wait(bar, parity);
@@ -233,54 +241,20 @@ __device__ void find_range(Smem<kSplit>& sm, const Params& p, int worker) {
   }
 }
 
-// ---------------------------------------------------------------- TMA producers
-// The tiles of a range in order.
-struct Cursor {
-  Walk w;
-  int tile, n;  // tile of the piece; items of the tile
-  __device__ Cursor(const Batch& q, Place from, Place to) : w(q, from, to), tile(0) { settle(); }
-  __device__ void settle() {
-    while (w.valid() && w.tiles() == 0) w.next();
-    n = w.valid() ? min(kTilePages, w.k1 - w.at.k - tile * kTilePages) : 0;
-  }
-  __device__ bool valid() const { return n > 0; }
-  __device__ void next() {
-    if (++tile == w.tiles()) {
-      tile = 0;
-      w.next();
-    }
-    settle();
-  }
-};
-
-// An item as the loads need it, held by lane i for item i of a tile.
-struct ItemLoad {
-  int phys, y, m;  // page, first row of the box, tensor map
-  int lo, hi;      // columns of the scores that are visible
-};
-
-// The table lookup of lane i's item; nothing waits for it before it is used.
-template <typename Maps>
-__device__ __forceinline__ ItemLoad item_load(const Params& p, const Cursor& c, int lane) {
-  constexpr int kWhole = sizeof(Maps) / sizeof(CUtensorMap) - 1;
-  ItemLoad t{p.num_blocks, 0, kWhole, 0, 0};
-  if (lane < c.n) {
-    const Item it = item_of(p.q.vis, c.w.position(), c.w.at.k + c.tile * kTilePages + lane);
-    t.phys = p.block_table[(long long)c.w.at.b * p.max_blocks + it.page];
-    t.lo = 0;
-    t.hi = it.b - it.a;
-    if (it.a == 0) {  // rows past the range fall behind the page's top, negative rows arrive as zeros
-      t.y = it.b - kPage;
-      t.lo = kPage - it.b;
-      t.hi = kPage;
-    } else {
-      t.y = it.a;
-      if (it.b < kPage) t.m = it.b - 1;  // only with a map for every end, see chunk_tc_impl
-    }
-  }
-  return t;
+// ---------------------------------------------------------------- tile records
+// Record i of the ring: false if the wait ran out.  A warp that has copied what
+// it needs releases it.
+template <bool kSplit>
+__device__ __forceinline__ bool wait_tile(Smem<kSplit>& sm, int i, uint64_t wns) {
+  return warp_wait(&sm.tile_full[i % kTiles], (i / kTiles) & 1, 42, wns);
+}
+template <bool kSplit>
+__device__ __forceinline__ void release_tile(Smem<kSplit>& sm, int i, bool one) {
+  __syncwarp();
+  if (one) mbar_arrive(&sm.tile_empty[i % kTiles]);
 }
 
+// ---------------------------------------------------------------- TMA producers
 // Both CTAs' load warps arrive on every slot, also where a CTA has nothing to
 // load (a tile of one or two items): the MMAs never run more than a ring ahead
 // of either, so a phase of `empty` is always seen before the next one ends.
@@ -306,11 +280,11 @@ struct Loader {
   __device__ bool ready() {
     return use == 0 || warp_wait(&sm.empty[sl], (use - 1) & 1, 40, p.wait_ns);
   }
-  // the 9 key slabs of a tile of n items of token `tok`
-  __device__ bool keys(const ItemLoad& it, int n, int tok) {
-    const int phys[2] = {__shfl_sync(0xffffffffu, it.phys, 2 * rank), __shfl_sync(0xffffffffu, it.phys, 2 * rank + 1)};
+  // the 9 key slabs of a tile of n items of token `tok`; lane i holds item i
+  __device__ bool keys(int3 it, int n, int tok) {
+    const int phys[2] = {__shfl_sync(0xffffffffu, it.x, 2 * rank), __shfl_sync(0xffffffffu, it.x, 2 * rank + 1)};
     const int y[2] = {__shfl_sync(0xffffffffu, it.y, 2 * rank), __shfl_sync(0xffffffffu, it.y, 2 * rank + 1)};
-    const int m[2] = {__shfl_sync(0xffffffffu, it.m, 2 * rank), __shfl_sync(0xffffffffu, it.m, 2 * rank + 1)};
+    const int m[2] = {__shfl_sync(0xffffffffu, it.z, 2 * rank), __shfl_sync(0xffffffffu, it.z, 2 * rank + 1)};
 #pragma unroll 1
     for (int e = 0; e < kSlabs; ++e, step()) {
       if (!mine()) continue;
@@ -329,11 +303,11 @@ struct Loader {
     return true;
   }
   // the value columns of a tile of n items: per item two blocks of 256 columns
-  __device__ bool values(const ItemLoad& it, int n) {
+  __device__ bool values(int3 it, int n) {
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int phys = __shfl_sync(0xffffffffu, it.phys, i), y = __shfl_sync(0xffffffffu, it.y, i),
-                m = __shfl_sync(0xffffffffu, it.m, i);
+      const int phys = __shfl_sync(0xffffffffu, it.x, i), y = __shfl_sync(0xffffffffu, it.y, i),
+                m = __shfl_sync(0xffffffffu, it.z, i);
 #pragma unroll 1
       for (int j = 0; j < 2; ++j, step()) {
         if (!mine()) continue;
@@ -355,97 +329,116 @@ struct Loader {
 
 template <bool kSplit, typename Maps>
 __device__ void load_role(Smem<kSplit>& sm, const Maps& pool, const CUtensorMap* qlo, const Params& p, int me, int rank,
-                          int worker, int lane) {
+                          int lane) {
   Loader<kSplit, Maps> ld{sm, pool, qlo, p, me, rank, elect_one()};
-  Cursor c(p.q, sm.from, sm.to);
-  ItemLoad next = item_load<Maps>(p, c, lane), prev{};
-  int n_prev = 0, i = 0;
+  int3 prev = make_int3(0, 0, 0);
+  int n_prev = 0;
   bool ok = true;
-  while (ok && c.valid()) {
-    ItemLoad it = next;
-    const int n = c.n, tok = c.w.token(), b = c.w.at.b;
-    Tile t;
-    t.n = n;
-    t.first = c.tile == 0;
-    t.last = c.tile + 1 == c.w.tiles();
-    t.whole = c.w.whole();
-    t.tok = tok;
-    t.slot = 2 * worker + (c.w.at.k > 0 ? 0 : 1);
-    c.next();
-    next = item_load<Maps>(p, c, lane);
-    if (lane < n && (it.phys < 0 || it.phys >= p.num_blocks)) {
-      if (me == 0 && rank == 0) report(MLA_ERR_BOUNDS, 22, b, it.phys);
-      it.phys = p.num_blocks;  // outside the pool: arrives as zeros, and is not visible
-      it.lo = it.hi = 0;
-    }
-    if (me == 0) {
-      Tile& d = sm.tile[i % kTiles];
-      if (lane < kTilePages) {
-        d.lo[lane] = it.lo;
-        d.hi[lane] = it.hi;
-      }
-      if (lane == 0) {
-        d.n = t.n;
-        d.first = t.first;
-        d.last = t.last;
-        d.whole = t.whole;
-        d.tok = t.tok;
-        d.slot = t.slot;
-      }
-      __syncwarp();
-      if (ld.one) mbar_arrive(&sm.tile_full[i % kTiles]);
-      __syncwarp();
-    }
+  for (int i = 0;; ++i) {
+    ok = ok && wait_tile(sm, i, p.wait_ns);
+    if (!ok) break;
+    const Tile& t = sm.tile[i % kTiles];
+    const int n = uni(t.n), tok = uni(t.tok), k = lane % kTilePages;
+    const int3 it = make_int3(t.phys[k], t.y[k], t.map[k]);
+    if (n == 0) break;
+    release_tile(sm, i, ld.one);
     ok = ld.keys(it, n, tok) && ld.values(prev, n_prev) && !aborted(sm);
     prev = it;
     n_prev = n;
-    ++i;
-  }
-  if (me == 0) {
-    if (lane == 0) sm.tile[i % kTiles].n = 0;
-    __syncwarp();
-    if (ld.one) mbar_arrive(&sm.tile_full[i % kTiles]);
-    __syncwarp();
   }
   if (ok) ok = ld.values(prev, n_prev);
   if (!ok) set_abort(sm);
 }
 
-// Record i: false if the wait ran out.
-template <bool kSplit>
-__device__ __forceinline__ bool wait_tile(Smem<kSplit>& sm, int i, uint64_t wns) {
-  return warp_wait(&sm.tile_full[i % kTiles], (i / kTiles) & 1, 42, wns);
-}
-
-// The queries of the pieces, one at a time; and, as no other warp meets them,
-// the rows of tokens that see nothing: zeros, log-sum-exp of an empty set.
-template <bool kSplit>
-__device__ void query_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, int rank, int lane) {
+// Walks the range: plans the tiles, loads a piece's queries once the scores of
+// the one before are done, and, as no other warp meets them, writes the rows of
+// tokens that see nothing (zeros, log-sum-exp of an empty set).
+template <bool kSplit, typename Maps>
+__device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, int rank, int worker, int lane) {
+  constexpr int kWhole = sizeof(Maps) / sizeof(CUtensorMap) - 1;
   const bool one = elect_one();
-  int n = 0;
+  int pieces = 0, i = 0;
+  const auto slot_free = [&] {
+    return i < kTiles || warp_wait(&sm.tile_empty[i % kTiles], (i / kTiles - 1) & 1, 43, p.wait_ns);
+  };
   for (Walk w(p.q, sm.from, sm.to); w.valid(); w.next()) {
-    const int tok = w.token();
-    if (w.tiles() == 0) {
+    const int tok = w.token(), nt = w.tiles();
+    if (nt == 0) {
       const long long row = (long long)tok * kH + kHalfH * rank;
       uint4* dst = reinterpret_cast<uint4*>(p.o_lat + row * kDc);
-      for (int i = lane; i < kHalfH * kDc / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+      for (int k = lane; k < kHalfH * kDc / 8; k += 32) dst[k] = make_uint4(0, 0, 0, 0);
       if (p.lse != nullptr)
         for (int h = lane; h < kHalfH; h += 32) p.lse[row + h] = -INFINITY;
       __syncwarp();
       continue;
     }
-    if (n >= 1 && !warp_wait(&sm.q_empty, (n - 1) & 1, 41, p.wait_ns)) {
-      set_abort(sm);
-      return;
+    for (int t = 0; t < nt; ++t, ++i) {
+      const int k0 = w.at.k + t * kTilePages, n = min(kTilePages, w.k1 - k0);
+      int phys = p.num_blocks, y = 0, m = kWhole, lo = 0, hi = 0;
+      if (lane < n) {
+        const Item it = item_of(p.q.vis, w.position(), k0 + lane);
+        phys = p.block_table[(long long)w.at.b * p.max_blocks + it.page];
+        if (it.a == 0) {  // rows past the range fall behind the page's top, negative rows arrive as zeros
+          y = it.b - kPage;
+          lo = kPage - it.b;
+          hi = kPage;
+        } else {
+          y = it.a;
+          hi = it.b - it.a;
+          if (it.b < kPage) m = it.b - 1;  // only with a map for every end, see chunk_tc_impl
+        }
+        if (phys < 0 || phys >= p.num_blocks) {
+          if (rank == 0) report(MLA_ERR_BOUNDS, 22, w.at.b, phys);
+          phys = p.num_blocks;  // outside the pool: arrives as zeros, and is not visible
+          lo = hi = 0;
+        }
+      }
+      if (!slot_free()) {
+        set_abort(sm);
+        return;
+      }
+      Tile& d = sm.tile[i % kTiles];
+      if (lane < kTilePages) {
+        d.phys[lane] = phys;
+        d.y[lane] = y;
+        d.map[lane] = m;
+        d.lo[lane] = lo;
+        d.hi[lane] = hi;
+      }
+      if (one) {
+        d.n = n;
+        d.first = t == 0;
+        d.last = t == nt - 1;
+        d.whole = w.whole();
+        d.tok = tok;
+        d.slot = 2 * worker + (w.at.k > 0 ? 0 : 1);
+      }
+      __syncwarp();
+      if (one) mbar_arrive(&sm.tile_full[i % kTiles]);
+      __syncwarp();
+      if (t > 0) continue;
+      if (pieces >= 1 && !warp_wait(&sm.q_empty, (pieces - 1) & 1, 41, p.wait_ns)) {
+        set_abort(sm);
+        return;
+      }
+      if (one) {
+        if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kSlabs * kSlab);
+        for (int e = 0; e < kSlabs; ++e)
+          tma_load_2d_pair(sm.q[e], qmap, 64 * e, tok * kH + kHalfH * rank, leader(&sm.q_full));
+      }
+      __syncwarp();
+      ++pieces;
     }
-    if (one) {
-      if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kSlabs * kSlab);
-      for (int e = 0; e < kSlabs; ++e)
-        tma_load_2d_pair(sm.q[e], qmap, 64 * e, tok * kH + kHalfH * rank, leader(&sm.q_full));
-    }
-    __syncwarp();
-    ++n;
   }
+  if (!slot_free()) {
+    set_abort(sm);
+    return;
+  }
+  if (one) {
+    sm.tile[i % kTiles].n = 0;
+    mbar_arrive(&sm.tile_full[i % kTiles]);
+  }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- MMA issuer (leader CTA)
@@ -534,6 +527,7 @@ __device__ void mma_role(Smem<kSplit>& sm, uint32_t tmem, const Params& p) {
     const int n = uni(t.n);
     const bool first = uni(t.first), last = uni(t.last);
     if (n == 0) break;
+    release_tile(sm, i, is.one);
     ok = is.scores(i, first, last) && (i == 0 || is.values(i - 1, n_prev, first_prev));
     n_prev = n;
     first_prev = first;
@@ -569,86 +563,91 @@ template <bool kSplit>
 struct Softmax {
   Smem<kSplit>& sm;
   const Params& p;
+  const CUtensorMap* omap;         // o_lat
+  const CUtensorMap* partmap;      // the workspace's pieces
   const uint32_t tl;               // this warp's TMEM lane quarter
   const int lane, l, half, ch, head;
-  int n_out = 0;                   // pieces written (parity of lbar)
+  const bool one;                  // the issuing lane
 
-  // A finished piece: its row sum (this thread's share), its maximum (in units
-  // of the raw scores) and where it goes.
+  // A piece whose output is in TMEM: its row sum, its maximum (in units of the
+  // raw scores) and where it goes.
   struct Piece {
-    float lsum, m;
+    float sum, m;
     int tok, slot, whole;
+    __device__ float inv() const { return sum == 0.f ? 0.f : 1.f / sum; }  // no visible row: zero (a NaN sum stays NaN)
   };
 
-  // The piece's factor 1 / l and log2-sum-exp, from the shares of the head's four threads.
-  __device__ bool total(const Piece& d, float& inv) {
-    float(&xl)[2][128] = sm.xl[n_out & 1];
-    xl[ch][l] = d.lsum;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.lbar);
-    if (!warp_wait(&sm.lbar, n_out & 1, 60, p.wait_ns)) return false;
-    ++n_out;
-    // the same order of additions in all four threads of the head
+  // The row sum of this thread's head from the shares of its four threads, in
+  // one order for all of them.
+  __device__ float row_sum(const float (&xl)[2][128]) const {
     const int l0 = l & 63;
-    const float tot = (xl[0][l0] + xl[1][l0]) + (xl[0][l0 + 64] + xl[1][l0 + 64]);
-    inv = tot == 0.f ? 0.f : 1.f / tot;  // no visible row: zero (a NaN sum stays NaN)
-    if (half == 0 && ch == 0) {
-      const float lse = tot == 0.f ? -INFINITY : fmaf(d.m, p.scale_log2, log2f(tot));
-      if (!d.whole) p.part_lse[(long long)d.slot * kH + head] = lse;
-      else if (p.lse != nullptr) p.lse[(long long)d.tok * kH + head] = lse;
-    }
-    return true;
+    return (xl[0][l0] + xl[1][l0]) + (xl[0][l0 + 64] + xl[1][l0 + 64]);
+  }
+  __device__ void store_lse(const Piece& d) {
+    if (half != 0 || ch != 0) return;
+    const float lse = d.sum == 0.f ? -INFINITY : fmaf(d.m, p.scale_log2, log2f(d.sum));
+    if (!d.whole) p.part_lse[(long long)d.slot * kH + head] = lse;
+    else if (p.lse != nullptr) p.lse[(long long)d.tok * kH + head] = lse;
   }
 
-  // This thread's 128 output columns [256 ch + 128 half, + 128) of its head.
-  // A whole token's are read out and rounded to registers first (the next
-  // tile's P V may then begin) and written by store_whole; a part's go to the
-  // workspace at once.
-  __device__ void read_whole(float inv, uint32_t (&out)[64]) {
+  // The finished piece's output: this warp's 32 heads x 128 columns (256 ch +
+  // 128 half on), a lane a head, go out through the warp's own 4 KiB of the P
+  // buffer (free until this tile's P is written there) by bulk tensor stores: a
+  // whole token's in bf16 to o_lat, 64 columns a pass, a part's in fp32 to the
+  // workspace, 32 columns a pass.  Plain stores, a row to a lane, kept the warps
+  // 2.8 us a token; here the tensor pipe computes the next tile's scores meanwhile.
+  __device__ void put(uint8_t* own, const uint32_t (&v)[32], const CUtensorMap* map, int x, int y) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[32];
-      tmem_ld32(tl + kTmemO + 128 * ch + 32 * c, o);
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        out[16 * c + k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-    }
-  }
-  __device__ void store_whole(int tok, const uint32_t (&out)[64]) {
-    uint4* dst = reinterpret_cast<uint4*>(p.o_lat + ((long long)tok * kH + head) * kDc + 256 * ch + 128 * half);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) dst[k] = make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
-  }
-  __device__ void write_part(int slot, float inv) {
-    float* part = p.part_o + ((long long)slot * kH + head) * kDc + 256 * ch + 128 * half;
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[32];
-      tmem_ld32(tl + kTmemO + 128 * ch + 32 * c, o);
-      tmem_wait_ld();
-      const float* f = reinterpret_cast<const float*>(o);
-      float4* dst = reinterpret_cast<float4*>(part + 32 * c);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        dst[k] = make_float4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
-    }
-  }
-
-  __device__ void arrive_p() {
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<uint4*>(own + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+          make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
     fence_proxy_async_smem();
-    tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_remote(leader(&sm.p_full));
+    if (one) {
+      tma_store_2d(map, own, x, y);
+      bulk_commit_group();
+      bulk_wait_read_all();
+    }
+    __syncwarp();
+  }
+  __device__ void write_out(uint8_t* own, const Piece& d) {
+    const float inv = d.inv();
+    const int col = 256 * ch + 128 * half, row0 = head - lane;  // the warp's first head
+    if (d.whole) {
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t a[32];
+          tmem_ld32(tl + kTmemO + 128 * ch + 64 * c + 32 * e, a);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            v[16 * e + k] = pack_bf16x2(__uint_as_float(a[2 * k]) * inv, __uint_as_float(a[2 * k + 1]) * inv);
+        }
+        put(own, v, omap, col + 64 * c, d.tok * kH + row0);
+      }
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tl + kTmemO + 128 * ch + 32 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * inv);
+        put(own, v, partmap, col + 32 * c, d.slot * kH + row0);
+      }
+    }
+    tc_fence_before();
   }
 
   __device__ bool run() {
     float m_used = -INFINITY, lsum = 0.f;
     Piece open{0.f, 0.f, 0, 0, 0};
-    uint32_t out[64];
     int i = 0;
-    const int q = 2 * half + ch;  // this warp's item of every tile
-    uint8_t* row = sm.p[q] + (l & 63) * 128;
+    const int q = 2 * half + ch;                        // this warp's item of every tile
+    uint8_t* own = sm.p[q] + ((l & 63) - lane) * 128;   // its 32 rows of the item's P slab
     for (;; ++i) {
       if (!wait_tile(sm, i, p.wait_ns)) return false;
       const Tile& t = sm.tile[i % kTiles];
@@ -656,7 +655,8 @@ struct Softmax {
       if (n == 0) break;
       const bool first = uni(t.first);
       const int lo = uni(t.lo[q]), hi = uni(t.hi[q]);
-      const int tok = t.tok, slot = t.slot, whole = t.whole;
+      const int tok = uni(t.tok), slot = uni(t.slot), whole = uni(t.whole);
+      release_tile(sm, i, one);
       if (!warp_wait(&sm.s_full[i & 1], (i >> 1) & 1, 62, p.wait_ns)) return false;
       tc_fence_after();
       float s[64];
@@ -681,15 +681,16 @@ struct Softmax {
         for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
       }
       tc_fence_before();
+      const bool close = first && i > 0;  // another piece's output is still in TMEM
       sm.xm[i & 1][ch][l] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (close) sm.xl[i & 1][ch][l] = lsum;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.xbar[i & 1]);
       if (!warp_wait(&sm.xbar[i & 1], (i >> 1) & 1, 63, p.wait_ns)) return false;
       const float m_tile = fmaxf(fmaxf(sm.xm[i & 1][0][l], sm.xm[i & 1][1][l]),
                                  fmaxf(sm.xm[i & 1][0][l ^ 64], sm.xm[i & 1][1][l ^ 64]));
-      const bool close = first && i > 0;  // another piece's output is still in TMEM
       if (first) {
-        open.lsum = lsum;
+        if (close) open.sum = row_sum(sm.xl[i & 1]);
         open.m = m_used;
         m_used = -INFINITY;
         lsum = 0.f;
@@ -743,46 +744,40 @@ struct Softmax {
         }
         tmem_wait_st();
       }
-      // row hl of the item's P slab, K-major with the 128-byte swizzle
+      if (close) {
+        write_out(own, open);
+        store_lse(open);
+      }
+      // row l mod 64 of the item's P slab, K-major with the 128-byte swizzle
       if (q < n) {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(row + ((c ^ (l & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(own + lane * 128 + ((c ^ (lane & 7)) << 4)) =
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       }
-      if (close) {
-        float inv;
-        if (!total(open, inv)) return false;
-        if (open.whole) {
-          read_whole(inv, out);
-          arrive_p();
-          store_whole(open.tok, out);
-        } else {
-          write_part(open.slot, inv);
-          arrive_p();
-        }
-      } else {
-        arrive_p();
-      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(leader(&sm.p_full));
       if (first) {
         open.tok = tok;
         open.slot = slot;
         open.whole = whole;
       }
     }
-    if (i > 0) {
-      open.lsum = lsum;
-      open.m = m_used;
-      float inv;
-      if (!warp_wait(&sm.pv_done, (i - 1) & 1, 65, p.wait_ns) || !total(open, inv)) return false;
+    if (i > 0) {  // the last piece
+      sm.xl[i & 1][ch][l] = lsum;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.lbar);
+      if (!warp_wait(&sm.lbar, 0, 60, p.wait_ns) || !warp_wait(&sm.pv_done, (i - 1) & 1, 65, p.wait_ns)) return false;
       tc_fence_after();
-      if (open.whole) {
-        read_whole(inv, out);
-        store_whole(open.tok, out);
-      } else {
-        write_part(open.slot, inv);
-      }
+      open.sum = row_sum(sm.xl[i & 1]);
+      open.m = m_used;
+      store_lse(open);
+      write_out(own, open);
     }
+    if (one) bulk_wait_all();
+    __syncwarp();
     return true;
   }
 };
@@ -791,7 +786,8 @@ struct Softmax {
 template <bool kSplit, typename Maps>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_pair_kernel(const __grid_constant__ Maps pool, const __grid_constant__ CUtensorMap qmap,
-                      const __grid_constant__ CUtensorMap qlomap, const __grid_constant__ Params p) {
+                      const __grid_constant__ CUtensorMap qlomap, const __grid_constant__ CUtensorMap omap,
+                      const __grid_constant__ CUtensorMap partmap, const __grid_constant__ Params p) {
   using G = Geo<kSplit>;
   extern __shared__ uint8_t smem_raw[];
   Smem<kSplit>& sm =
@@ -813,7 +809,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&sm.p_full, 2 * kSoftmaxWarps);
     mbar_init(&sm.pv_done, 1);
     mbar_init(&sm.lbar, kSoftmaxWarps);
-    for (int b = 0; b < kTiles; ++b) mbar_init(&sm.tile_full[b], 1);
+    for (int b = 0; b < kTiles; ++b) {
+      mbar_init(&sm.tile_full[b], 1);
+      mbar_init(&sm.tile_empty[b], kSoftmaxWarps + kLoadWarps + (rank == 0 ? 1 : 0));  // the MMA warp works in rank 0
+    }
     mbar_init(&sm.fin, 1);
     sm.abort_flag = 0;
     fence_mbar_init();
@@ -844,15 +843,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp < kSoftmaxWarps) {
     const int l = (warp & 3) * 32 + lane;
-    Softmax<kSplit> so{sm, p, tmem + ((uint32_t)((warp & 3) * 32) << 16), lane, l, l >> 6, warp >> 2,
-                       kHalfH * rank + (l & 63)};
+    Softmax<kSplit> so{sm, p, &omap, &partmap, tmem + ((uint32_t)((warp & 3) * 32) << 16), lane, l, l >> 6, warp >> 2,
+                       kHalfH * rank + (l & 63), elect_one()};
     if (!so.run()) set_abort(sm);
   } else if (warp == kMmaWarp) {
     if (rank == 0) mma_role(sm, tmem, p);
   } else if (warp == kQueryWarp) {
-    query_role(sm, &qmap, p, rank, lane);
+    plan_role<kSplit, Maps>(sm, &qmap, p, rank, worker, lane);
   } else {
-    load_role<kSplit, Maps>(sm, pool, &qlomap, p, warp - kLoadWarp0, rank, worker, lane);
+    load_role<kSplit, Maps>(sm, pool, &qlomap, p, warp - kLoadWarp0, rank, lane);
   }
 
   tc_fence_before();
@@ -938,6 +937,20 @@ inline mla_status pool_map(const mla_cache* k, CUtensorMap* map, int rows) {
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k->pool, dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_CUDA;
+}
+
+// Rows of 512 values, stored in boxes of 32 rows x 128 bytes: o_lat (bf16) or
+// the workspace's pieces (fp32).
+inline mla_status out_map(void* p, long long rows, CUtensorMapDataType type, int elem, CUtensorMap* map) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (enc == nullptr) return MLA_ERR_CUDA;
+  const cuuint64_t dims[2] = {(cuuint64_t)kDc, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kDc * elem};
+  const cuuint32_t box[2] = {128u / elem, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, type, 2, p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_CUDA;
 }
 

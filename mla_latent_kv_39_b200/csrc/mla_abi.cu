@@ -462,21 +462,22 @@ int chunk_workers(int max_workers) {
   return max_workers > 0 ? std::min(max_workers, most) : most;
 }
 
-template <bool kSplit, typename Maps>
-mla_status chunk_pair_launch(const Maps& pool, const CUtensorMap& q, const CUtensorMap& qlo, const chunk::Params& p,
-                             cudaStream_t s) {
-  static std::atomic<uint64_t> attr{0};
-  constexpr size_t smem = chunk::smem_bytes<kSplit>();
-  MLA_TRY(pairdec::set_smem_once((const void*)chunk::chunk_pair_kernel<kSplit, Maps>, smem, attr));
-  return st(launch_chained(chunk::chunk_pair_kernel<kSplit, Maps>, dim3(2 * p.workers), dim3(chunk::kThreads), smem, s,
-                           pool, q, qlo, p));
-}
-
 template <typename Maps>
 mla_status chunk_pool_maps(const mla_cache* k, Maps* maps) {
   constexpr int n = sizeof(Maps) / sizeof(CUtensorMap);
   for (int i = 0; i < n; ++i) MLA_TRY(chunk::pool_map(k, &maps->end[i], n == 1 ? chunk::kPage : i + 1));
   return MLA_OK;
+}
+
+template <bool kSplit, typename Maps>
+mla_status chunk_pair_launch(const mla_cache* k, const CUtensorMap (&m)[4], const chunk::Params& p, cudaStream_t s) {
+  Maps pool;
+  MLA_TRY(chunk_pool_maps(k, &pool));
+  static std::atomic<uint64_t> attr{0};
+  constexpr size_t smem = chunk::smem_bytes<kSplit>();
+  MLA_TRY(pairdec::set_smem_once((const void*)chunk::chunk_pair_kernel<kSplit, Maps>, smem, attr));
+  return st(launch_chained(chunk::chunk_pair_kernel<kSplit, Maps>, dim3(2 * p.workers), dim3(chunk::kThreads), smem, s,
+                           pool, m[0], m[1], m[2], m[3], p));
 }
 
 mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch& b, const mla_cache* k, int workers,
@@ -487,19 +488,18 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
   const chunk::Params p{b, k->block_table, k->max_blocks_per_seq, k->num_blocks, scale_of(c) * 1.4426950408889634f, g_wait_limit_ns.load(std::memory_order_relaxed), workers,
                         reinterpret_cast<int4*>(base + L.off_piece), reinterpret_cast<float*>(base + L.off_lse),
                         reinterpret_cast<float*>(base + L.off_o), o_lat, lse};
-  CUtensorMap qmap, qlo;
-  MLA_TRY(pairdec::query_map(q, b.n_tok, &qmap));
-  MLA_TRY(pairdec::query_map(split ? q + (long long)b.n_tok * chunk::kH * chunk::kRow : q, b.n_tok, &qlo));
+  CUtensorMap m[4];  // queries, their low parts, output, pieces
+  MLA_TRY(pairdec::query_map(q, b.n_tok, &m[0]));
+  MLA_TRY(pairdec::query_map(split ? q + (long long)b.n_tok * chunk::kH * chunk::kRow : q, b.n_tok, &m[1]));
+  MLA_TRY(chunk::out_map(o_lat, (long long)b.n_tok * chunk::kH, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, &m[2]));
+  MLA_TRY(chunk::out_map(p.part_o, 2LL * workers * chunk::kH, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, &m[3]));
   // only a window shorter than a page cuts a page's rows on both sides
-  if (b.vis.window > 0 && b.vis.window < chunk::kPage) {
-    chunk::PoolMaps maps;
-    MLA_TRY(chunk_pool_maps(k, &maps));
-    MLA_TRY(split ? chunk_pair_launch<true>(maps, qmap, qlo, p, s) : chunk_pair_launch<false>(maps, qmap, qlo, p, s));
-  } else {
-    chunk::PoolMap map;
-    MLA_TRY(chunk_pool_maps(k, &map));
-    MLA_TRY(split ? chunk_pair_launch<true>(map, qmap, qlo, p, s) : chunk_pair_launch<false>(map, qmap, qlo, p, s));
-  }
+  if (b.vis.window > 0 && b.vis.window < chunk::kPage)
+    MLA_TRY((split ? chunk_pair_launch<true, chunk::PoolMaps>(k, m, p, s)
+                   : chunk_pair_launch<false, chunk::PoolMaps>(k, m, p, s)));
+  else
+    MLA_TRY((split ? chunk_pair_launch<true, chunk::PoolMap>(k, m, p, s)
+                   : chunk_pair_launch<false, chunk::PoolMap>(k, m, p, s)));
   return st(launch_chained(chunk::chunk_merge_kernel, dim3(workers, chunk::kH / chunk::kMergeHeads), dim3(256), 0, s,
                            workers, (const int4*)p.piece, (const float*)p.part_lse, (const float*)p.part_o, o_lat, lse));
 }
