@@ -106,8 +106,6 @@ struct Smem {
   Tile tile[kTiles];
   float xm[2][2][128];                       // [tile parity][column half] maximum of each lane's columns
   float xl[2][2][128];                       // [tile parity][column half] shares of a finished piece's row sums
-  long long warp_sum[kThreads / 32];
-  Place from, to;                            // this worker's range
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -125,13 +123,13 @@ static_assert(sizeof(long long) * (kMaxBatch + 1) <= 4 * (kKvSlot + kSlab) &&
 // earlier worker, 1: the beginning of a token that a later one goes on with).
 struct Layout {
   int workers;
-  long long off_piece, off_lse, off_o, total;
+  long long off_shares, off_lse, off_o, total;
 };
 inline Layout layout(int workers) {
   Layout L{};
   L.workers = workers;
   size_t o = 0;
-  L.off_piece = o; o = align_up(o + sizeof(int4) * (size_t)workers, 256);
+  L.off_shares = o; o = align_up(o + sizeof(int4) * (size_t)workers, 256);
   L.off_lse = o;   o = align_up(o + sizeof(float) * 2 * (size_t)workers * kH, 256);
   L.off_o = o;     o = align_up(o + sizeof(float) * 2 * (size_t)workers * kH * kDc, 256);
   L.total = o;
@@ -145,7 +143,8 @@ struct Params {
   float scale_log2;
   unsigned long long wait_ns;
   int workers;
-  int4* piece;      // a worker's Shares
+  float inv_workers;
+  int4* shares;     // the workers' Shares
   float* part_lse;
   float* part_o;
   bf16* o_lat;
@@ -206,39 +205,66 @@ __device__ __forceinline__ bool aborted(Smem<kSplit>& sm) {
 }
 
 // ---------------------------------------------------------------- the cut
-// Costs of the sequences, summed up in shared memory by all threads; then the
-// two ends of this worker's range.
-template <bool kSplit>
-__device__ void find_range(Smem<kSplit>& sm, const Params& p, int worker) {
-  long long* C = reinterpret_cast<long long*>(sm.ring);
+__device__ __forceinline__ long long shfl64(long long v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
+__device__ __forceinline__ Found found_of(const Found& f, int lane) {
+  Found r;
+  r.at = {__shfl_sync(0xffffffffu, f.at.b, lane), __shfl_sync(0xffffffffu, f.at.j, lane),
+          __shfl_sync(0xffffffffu, f.at.k, lane)};
+  r.s.t0 = __shfl_sync(0xffffffffu, f.s.t0, lane);
+  r.s.n = __shfl_sync(0xffffffffu, f.s.n, lane);
+  r.s.p0 = __shfl_sync(0xffffffffu, f.s.p0, lane);
+  r.s.state = Sequence::kFine;
+  r.base = shfl64(f.base, lane);
+  return r;
+}
+
+// The two ends of this worker's range, by one warp: costs of the sequences, a
+// run of them to a lane, summed up in `C` (shared memory); then lane 0 looks for
+// the one end and lane 1 for the other.
+__device__ __forceinline__ Cut find_range(const Params& p, long long* C, int worker, int lane, Found& from, Found& to) {
   const Batch& q = p.q;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (q.batch + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, q.batch), b1 = min(b0 + per, q.batch);
-  long long mine = 0;
+  const int per = (q.batch + 31) / 32, b0 = min(lane * per, q.batch), b1 = min(b0 + per, q.batch);
+  Cut cut{0, p.workers, p.inv_workers, 0};
+  long long mine = 0, longest = 0;
+  long long own = 0;  // tokens of this lane's run
   for (int b = b0; b < b1; ++b) {
     const Sequence s = sequence_of(q, b);
     if (blockIdx.x == 0) report_sequence(q, b, s);
-    mine += cost_of_tokens(q.vis, s, s.n);
+    mine += cut.tokens(q.vis, s, s.n);
+    own += s.n;
+    longest = max(longest, longest_token(q.vis, s));
     C[b + 1] = mine;
   }
   long long x = mine;
+  long long t = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const long long u = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) {
+      x += y;
+      t += u;
+    }
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
   }
-  if (lane == 31) sm.warp_sum[warp] = x;
-  __syncthreads();
+  cut.total = shfl64(x, 31);
   long long ahead = x - mine;
-  for (int w = 0; w < warp; ++w) ahead += sm.warp_sum[w];
-  for (int b = b0; b < b1; ++b) C[b + 1] += ahead;
-  if (tid == 0) C[0] = 0;
-  __syncthreads();
-  if (warp < 2 && lane == 0) {
-    const Place at = cut(q, C, worker + warp, p.workers);
-    if (warp == 0) sm.from = at; else sm.to = at;
+  const long long tokens = shfl64(t, 31);
+  if (one_token_each(tokens, cut.total, longest, p.workers)) {
+    cut.single = 1;
+    cut.total = tokens;
+    ahead = t - own;
+    mine = 0;
+    for (int b = b0; b < b1; ++b) C[b + 1] = mine += sequence_of(q, b).n;
   }
+  for (int b = b0; b < b1; ++b) C[b + 1] += ahead;
+  if (lane == 0) C[0] = 0;
+  __syncwarp();
+  const Found f = place_at(q, cut, C, cut.at(worker + (lane & 1)));
+  from = found_of(f, 0);
+  to = found_of(f, 1);
+  __syncwarp();
+  return cut;
 }
 
 // ---------------------------------------------------------------- tile records
@@ -350,9 +376,10 @@ __device__ void load_role(Smem<kSplit>& sm, const Maps& pool, const CUtensorMap*
   if (!ok) set_abort(sm);
 }
 
-// Walks the range: plans the tiles, loads a piece's queries once the scores of
-// the one before are done, and, as no other warp meets them, writes the rows of
-// tokens that see nothing (zeros, log-sum-exp of an empty set).
+// Finds the worker's range and walks it: plans the tiles, loads a piece's
+// queries once the scores of the one before are done, and, as no other warp meets
+// them, writes the rows of tokens that see nothing (zeros, log-sum-exp of an
+// empty set) and what the merge needs to know.
 template <bool kSplit, typename Maps>
 __device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, int rank, int worker, int lane) {
   constexpr int kWhole = sizeof(Maps) / sizeof(CUtensorMap) - 1;
@@ -361,7 +388,23 @@ __device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Param
   const auto slot_free = [&] {
     return i < kTiles || warp_wait(&sm.tile_empty[i % kTiles], (i / kTiles - 1) & 1, 43, p.wait_ns);
   };
-  for (Walk w(p.q, sm.from, sm.to); w.valid(); w.next()) {
+  const auto give_up = [&] {  // nothing to merge
+    set_abort(sm);
+    if (rank == 0 && one) p.shares[worker] = make_int4(-1, -1, worker, -1);
+  };
+  const auto load_query = [&](int tok) {
+    if (one) {
+      if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kSlabs * kSlab);
+      for (int e = 0; e < kSlabs; ++e)
+        tma_load_2d_pair(sm.q[e], qmap, 64 * e, tok * kH + kHalfH * rank, leader(&sm.q_full));
+    }
+    __syncwarp();
+  };
+  Found from, to;
+  const Cut cut = find_range(p, reinterpret_cast<long long*>(sm.ring), worker, lane, from, to);
+  fence_proxy_async_smem();  // the prefix sums give way to the ring's loads
+  __syncwarp();
+  for (Walk w(p.q, from.at, from.s, to.at); w.valid(); w.next()) {
     const int tok = w.token(), nt = w.tiles();
     if (nt == 0) {
       const long long row = (long long)tok * kH + kHalfH * rank;
@@ -372,6 +415,7 @@ __device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Param
       __syncwarp();
       continue;
     }
+    if (pieces == 0) load_query(tok);
     for (int t = 0; t < nt; ++t, ++i) {
       const int k0 = w.at.k + t * kTilePages, n = min(kTilePages, w.k1 - k0);
       int phys = p.num_blocks, y = 0, m = kWhole, lo = 0, hi = 0;
@@ -393,10 +437,7 @@ __device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Param
           lo = hi = 0;
         }
       }
-      if (!slot_free()) {
-        set_abort(sm);
-        return;
-      }
+      if (!slot_free()) return give_up();
       Tile& d = sm.tile[i % kTiles];
       if (lane < kTilePages) {
         d.phys[lane] = phys;
@@ -416,28 +457,22 @@ __device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Param
       __syncwarp();
       if (one) mbar_arrive(&sm.tile_full[i % kTiles]);
       __syncwarp();
-      if (t > 0) continue;
-      if (pieces >= 1 && !warp_wait(&sm.q_empty, (pieces - 1) & 1, 41, p.wait_ns)) {
-        set_abort(sm);
-        return;
+      if (t == 0 && pieces++ > 0) {  // with the tile handed out, its query follows when the one before is done with
+        if (!warp_wait(&sm.q_empty, (pieces - 2) & 1, 41, p.wait_ns)) return give_up();
+        load_query(tok);
       }
-      if (one) {
-        if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, 2 * kSlabs * kSlab);
-        for (int e = 0; e < kSlabs; ++e)
-          tma_load_2d_pair(sm.q[e], qmap, 64 * e, tok * kH + kHalfH * rank, leader(&sm.q_full));
-      }
-      __syncwarp();
-      ++pieces;
     }
   }
-  if (!slot_free()) {
-    set_abort(sm);
-    return;
-  }
+  if (!slot_free()) return give_up();
   if (one) {
     sm.tile[i % kTiles].n = 0;
     mbar_arrive(&sm.tile_full[i % kTiles]);
   }
+  __syncwarp();
+  const Shares e = shares_of(p.q, cut, from, to, worker);
+  if (rank == 0 && one) p.shares[worker] = make_int4(e.continues, e.begins, e.last, e.first);
+  if (e.continues < 0)  // nothing of this worker's in its first place
+    for (int h = lane; h < kHalfH; h += 32) p.part_lse[2LL * worker * kH + kHalfH * rank + h] = -INFINITY;
   __syncwarp();
 }
 
@@ -825,21 +860,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&pool.end[sizeof(Maps) / sizeof(CUtensorMap) - 1]);
     prefetch_tensormap(&qmap);
   }
-  pdl_wait();  // the queries, the tables and the appended rows come from the kernels before
-  pdl_trigger();
-  find_range(sm, p, worker);
-  fence_proxy_async_smem();  // the prefix sums give way to the ring's loads
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers are initialised, their prefix sums read
+  cluster_sync();  // both CTAs' barriers are initialised
   tc_fence_after();
   const uint32_t tmem = uni(sm.tmem_base);
-  const Place from = sm.from, to = sm.to;
-
-  if (rank == 0 && threadIdx.x == 0) {
-    const Shares e = shares_of(p.q, from, to);
-    p.piece[worker] = make_int4(e.x, e.y, e.z, 0);
-  }
+  pdl_wait();  // the queries, the tables and the appended rows come from the kernels before
+  pdl_trigger();
 
   if (warp < kSoftmaxWarps) {
     const int l = (warp & 3) * 32 + lane;
@@ -866,62 +893,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- merge
 // Joins the pieces of the tokens that several workers share:
 //   o_lat = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).
-// Grid (workers, head groups): block (w, y) joins the token that worker w
-// begins and does not end; most workers have none.  Pieces are summed in the
-// order of the workers.  A thread owns 8 latent columns of one head.
-constexpr int kMergeHeads = 4;
-__global__ void __launch_bounds__(256) chunk_merge_kernel(int workers, const int4* __restrict__ piece,
-                                                          const float* __restrict__ part_lse,
-                                                          const float* __restrict__ part_o, bf16* __restrict__ o_lat,
-                                                          float* __restrict__ lse_out) {
+// Grid (workers, heads / 4).  A token of few pieces is joined by the blocks of
+// the worker that begins it, four heads to a block, one to each group of 64
+// threads.  Of a token of many pieces (a long request) the blocks of its first
+// four workers take a head each, its pieces dealt to the four groups: 128 blocks
+// that read 150 KB each of 74 pieces, against 32 with 600 KB.  A thread owns 8
+// latent columns; several loads are in flight, under no condition.  An idle
+// worker's place counts as a piece without visible rows (lse -inf).  Sums run in
+// a fixed order.
+constexpr int kMergeThreads = 256, kMergeGroups = kMergeThreads / 64, kMergeFew = 8;
+
+__global__ void __launch_bounds__(kMergeThreads, 6) chunk_merge_kernel(const int4* __restrict__ shares,
+                                                                    const float* __restrict__ part_lse,
+                                                                    const float* __restrict__ part_o,
+                                                                    bf16* __restrict__ o_lat,
+                                                                    float* __restrict__ lse_out) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int slots[kMaxWorkers + 1];
-  __shared__ int count;
-  const int w0 = blockIdx.x, tok = piece[w0].z;
-  if (tok < 0) return;
-  if (threadIdx.x < 32) {  // the workers behind w0 that go on with the token, up to the one that ends it
-    const int lane = threadIdx.x;
-    int n = 1;
-    if (lane == 0) slots[0] = 2 * w0 + 1;
-    for (int b = w0 + 1; b < workers; b += 32) {
-      const int4 e = b + lane < workers ? piece[b + lane] : make_int4(-1, 0, -1, 0);
-      const unsigned on = __ballot_sync(0xffffffffu, e.x == tok), end = __ballot_sync(0xffffffffu, e.x == tok && e.y);
-      if (e.x == tok) slots[n + __popc(on & ((1u << lane) - 1))] = 2 * (b + lane);
-      n += __popc(on);
-      if (end) break;
+  __shared__ float wt[kMergeGroups][kMaxWorkers];
+  __shared__ float4 sum[kMergeGroups][2][64];
+  const int w = blockIdx.x;
+  int4 own = shares[w];
+  int w0 = w;
+  if (own.y < 0 || own.z - w0 < kMergeFew) {  // not the first worker of a token of many pieces: one of its next?
+    if (own.w >= 0 && w - own.w < kMergeGroups) {
+      const int4 head = shares[own.w];
+      if (head.z - own.w >= kMergeFew) {
+        w0 = own.w;
+        own = head;
+      }
     }
-    if (lane == 0) count = n;
+  }
+  const int tok = own.y, n = own.z - w0 + 1;
+  if (tok < 0) return;
+  const bool many = n > kMergeFew;
+  const int group = threadIdx.x / 64, col = threadIdx.x % 64, lane = threadIdx.x & 31;
+  const int h = kMergeGroups * blockIdx.y + (many ? w - w0 : group);
+  const int list = many ? 0 : group;  // of many, one list of weights for all groups
+  // piece i: the beginning with worker w0, the rest with the workers behind it
+  const auto slot_of = [&](int i) { return 2 * (w0 + i) + (i == 0 ? 1 : 0); };
+  if (col < 32 && (!many || group == 0)) {
+    float M = -INFINITY, Z = 0.f;
+    for (int i = lane; i < n; i += 32) {
+      const float x = part_lse[(long long)slot_of(i) * kH + h];
+      wt[list][i] = x;
+      M = fmaxf(M, x);
+      if (x != x) Z = x;  // the maximum passes over NaN, the sum must not
+    }
+    M = warp_max(M);
+    for (int i = lane; i < n; i += 32) {
+      const float x = M == -INFINITY ? 0.f : exp2f(wt[list][i] - M);  // M = -inf: no piece has a visible row
+      wt[list][i] = x;
+      Z += x;
+    }
+    Z = warp_sum(Z);
+    const float inv = Z == 0.f ? 0.f : 1.f / Z;
+    for (int i = lane; i < n; i += 32) wt[list][i] *= inv;
+    if (lse_out != nullptr && lane == 0) lse_out[(long long)tok * kH + h] = Z == 0.f ? -INFINITY : M + log2f(Z);
   }
   __syncthreads();
-  const int n = count;
-  const int h = blockIdx.y * kMergeHeads + threadIdx.x / 64, d = 8 * (threadIdx.x % 64);
-  float M = -INFINITY, Z = 0.f;
-  bool nan = false;  // a maximum passes over NaN, the result must not
-  for (int i = 0; i < n; ++i) {
-    const float x = part_lse[(long long)slots[i] * kH + h];
-    M = fmaxf(M, x);
-    nan |= x != x;
-  }
-  if (nan) Z = NAN;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (M != -INFINITY) {  // else no piece has a visible row
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wt = exp2f(part_lse[(long long)slots[i] * kH + h] - M);
-      const float4* src = reinterpret_cast<const float4*>(part_o + ((long long)slots[i] * kH + h) * kDc + d);
-      const float4 x = __ldcs(src), y = __ldcs(src + 1);
-      Z += wt;
-      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  const auto add = [&](int i, const float4& x, const float4& y) {
+    const float f = i < n ? wt[list][i] : 0.f;
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = fmaf(wt, v[k], acc[k]);
+    for (int c = 0; c < 8; ++c) acc[c] = fmaf(f, f == 0.f ? 0.f : v[c], acc[c]);  // weight 0: nothing was written there
+  };
+  const auto at = [&](int i) {
+    return reinterpret_cast<const float4*>(part_o + ((long long)slot_of(min(i, n - 1)) * kH + h) * kDc + 8 * col);
+  };
+  const int step = many ? kMergeGroups : 1;
+  for (int i = many ? group : 0; i < n; i += 3 * step) {
+    const float4 x0 = __ldcs(at(i)), y0 = __ldcs(at(i) + 1);
+    const float4 x1 = __ldcs(at(i + step)), y1 = __ldcs(at(i + step) + 1);
+    if (n > 2) {
+      const float4 x2 = __ldcs(at(i + 2 * step)), y2 = __ldcs(at(i + 2 * step) + 1);
+      add(i, x0, y0);
+      add(i + step, x1, y1);
+      add(i + 2 * step, x2, y2);
+    } else {
+      add(i, x0, y0);
+      add(i + 1, x1, y1);
     }
   }
-  const float inv = Z == 0.f ? 0.f : 1.f / Z;
-  *reinterpret_cast<uint4*>(o_lat + ((long long)tok * kH + h) * kDc + d) =
-      make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                 pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-  if (lse_out != nullptr && d == 0) lse_out[(long long)tok * kH + h] = Z == 0.f ? -INFINITY : M + log2f(Z);
+  if (many) {
+    sum[group][0][col] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    sum[group][1][col] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int g = 1; g < kMergeGroups; ++g) {
+        const float4 v = sum[g][e][col];
+        acc[4 * e] += v.x;
+        acc[4 * e + 1] += v.y;
+        acc[4 * e + 2] += v.z;
+        acc[4 * e + 3] += v.w;
+      }
+  }
+  *reinterpret_cast<uint4*>(o_lat + ((long long)tok * kH + h) * kDc + 8 * col) =
+      make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                 pack_bf16x2(acc[6], acc[7]));
 }
 
 // ================================================================ host side

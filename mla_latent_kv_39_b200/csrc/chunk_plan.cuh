@@ -15,8 +15,8 @@
 // The number of items of a token is a sum of floors of its position, so the
 // items of a whole run of tokens have a closed form, and the cut of all work
 // into equal parts needs one prefix sum over the sequences, not over the
-// tokens: every CTA makes it for itself (8 bytes read per sequence) and there
-// is no planning launch ahead of the attention.
+// tokens: a warp of every CTA makes it for itself (8 bytes read per sequence) and
+// there is no planning launch ahead of the attention.
 #pragma once
 
 #include "common.cuh"
@@ -30,6 +30,9 @@ constexpr int kTilePages = 4;     // items of a tile of the tensor-core kernel
 // A token's fixed cost in items: its query load and epilogue, and the unused
 // part of its last tile.
 constexpr int kTokenCost = 3;
+// What cutting tokens into pieces costs the call, in items of one worker: pieces
+// written to the workspace and joined by another kernel (about 10 us, a tile 2.4).
+constexpr int kSplitCost = 16;
 
 struct Visible {
   int window, sinks;  // window = 0: all rows up to the token's own
@@ -126,9 +129,31 @@ __device__ __forceinline__ void report_sequence(const Batch& q, int b, const Seq
   if (s.state == Sequence::kBadLength) report(MLA_ERR_BOUNDS, 21, b, q.seq_lens[b]);
 }
 
-// Cost of the first n tokens of a sequence.
-__host__ __device__ inline long long cost_of_tokens(const Visible& vis, const Sequence& s, int n) {
-  return (long long)kTokenCost * n + (s.p0 >= 0 ? vis.items_of_run(s.p0, n) : 0);
+// How the work is cut.  `single`: a token to a worker, none split, for calls of
+// no more tokens than workers whose longest token is hardly longer than an equal
+// part (a decode step of similar lengths); otherwise equal parts of cost.
+struct Cut {
+  long long total;  // cost of all tokens (their number, if single)
+  int workers;
+  float inv;        // 1 / workers
+  int single;
+  __host__ __device__ long long tokens(const Visible& vis, const Sequence& s, int n) const {
+    return single ? n : (long long)kTokenCost * n + (s.p0 >= 0 ? vis.items_of_run(s.p0, n) : 0);
+  }
+  // The cost where the range of worker w begins (w = workers: where the last
+  // ends): growing in w, and the same for the worker that ends there.
+  __host__ __device__ long long at(int w) const {
+    if (w >= workers) return total;
+    if (single) return w < total ? w : total;
+    return (long long)((double)total * w * inv);
+  }
+};
+__host__ __device__ inline bool one_token_each(long long tokens, long long total, long long longest, int workers) {
+  return tokens <= workers && longest <= total / workers + kSplitCost;
+}
+// The longest cost that a token of the sequence may have.
+__host__ __device__ inline long long longest_token(const Visible& vis, const Sequence& s) {
+  return s.n > 0 && s.p0 >= 0 ? kTokenCost + vis.items(s.p0 + s.n - 1) + 1 : 0;
 }
 
 // A place in the order of all items: sequence, token within it, item.
@@ -140,34 +165,37 @@ __host__ __device__ inline bool before(const Place& x, const Place& y) {
 }
 
 // The place at cost x, given the costs C[0 .. batch] of the sequences before
-// each.  Inside a token it is moved back to a tile boundary.
-__host__ __device__ inline Place place_at(const Batch& q, const long long* C, long long x) {
-  if (x >= C[q.batch]) return {q.batch, 0, 0};
+// each; its sequence and the cost ahead of that.  Inside a token it is moved back
+// to a tile boundary.
+struct Found {
+  Place at;
+  Sequence s;
+  long long base;
+};
+__host__ __device__ inline Found place_at(const Batch& q, const Cut& cut, const long long* C, long long x) {
+  Found f{{q.batch, 0, 0}, {0, 0, -1, Sequence::kFine}, cut.total};
+  if (x >= cut.total) return f;
   int lo = 0, hi = q.batch - 1;  // the last sequence with C[b] <= x; it has tokens, as C[b + 1] > x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (C[mid] <= x) lo = mid; else hi = mid - 1;
   }
-  const Sequence s = sequence_of(q, lo);
-  const long long r = x - C[lo];
-  int a = 0, z = s.n - 1;
+  f.s = sequence_of(q, lo);
+  f.base = C[lo];
+  const long long r = x - f.base;
+  int a = 0, z = f.s.n - 1;
   while (a < z) {
     const int mid = (a + z + 1) >> 1;
-    if (cost_of_tokens(q.vis, s, mid) <= r) a = mid; else z = mid - 1;
+    if (cut.tokens(q.vis, f.s, mid) <= r) a = mid; else z = mid - 1;
   }
   int k = 0;
-  if (s.p0 >= 0) {
-    const long long i = r - cost_of_tokens(q.vis, s, a) - kTokenCost;
-    const int n = q.vis.items(s.p0 + a);
+  if (f.s.p0 >= 0 && !cut.single) {
+    const long long i = r - cut.tokens(q.vis, f.s, a) - kTokenCost;
+    const int n = q.vis.items(f.s.p0 + a);
     k = i <= 0 ? 0 : (int)(i < n ? i : n - 1) / kTilePages * kTilePages;
   }
-  return {lo, a, k};
-}
-
-// Where the range of worker w of `workers` begins (w = workers: where the last ends).
-__host__ __device__ inline Place cut(const Batch& q, const long long* C, int w, int workers) {
-  const long long total = C[q.batch];
-  return place_at(q, C, total / workers * w + total % workers * w / workers);
+  f.at = {lo, a, k};
+  return f;
 }
 
 // A value that all lanes of a warp hold, in the warp-uniform datapath.
@@ -186,10 +214,9 @@ struct Walk {
   Place at, to;
   Sequence s;
   int n_items, k1;  // items of the token; end of the piece
-  __host__ __device__ Walk(const Batch& q_, Place from, Place to_) : q(q_), at(from), to(to_), n_items(0), k1(0) {
-    s.n = 0;
-    if (!valid()) return;
-    load();
+  // `seq`: the sequence of `from`
+  __host__ __device__ Walk(const Batch& q_, Place from, Sequence seq, Place to_)
+      : q(q_), at(from), to(to_), s(seq), n_items(0), k1(0) {
     settle();
   }
   __host__ __device__ bool valid() const { return before(at, to); }
@@ -222,21 +249,36 @@ struct Walk {
   __host__ __device__ int tiles() const { return (k1 - at.k + kTilePages - 1) / kTilePages; }
 };
 
-// What a worker holds of tokens that it does not hold whole: x = the token that
-// its range continues (-1: none), y = 1 if that token ends in its range, z = the
-// token that its range begins and does not end (-1: none).
+// What worker w holds of tokens that it does not hold whole: the token that its
+// range continues (-1: none), the token that its range begins and does not end
+// (-1: none) and the last worker that holds a piece of that one; and, where its
+// range begins inside a token, the worker that begins that one (-1 otherwise).
+// Workers between the first and the last may be without work: they continue no
+// token.
 struct Shares {
-  int x, y, z;
+  int continues, begins, last, first;
 };
-__host__ __device__ inline Shares shares_of(const Batch& q, const Place& from, const Place& to) {
-  const bool same = from.b == to.b && from.j == to.j;
-  Shares e{-1, 0, -1};
-  if (!before(from, to)) return e;
-  if (from.k > 0) {
-    e.x = sequence_of(q, from.b).t0 + from.j;
-    e.y = same ? 0 : 1;
+__host__ __device__ inline Shares shares_of(const Batch& q, const Cut& cut, const Found& from, const Found& to, int w) {
+  const bool same = from.at.b == to.at.b && from.at.j == to.at.j, some = before(from.at, to.at);
+  Shares e{-1, -1, w, -1};
+  if (from.at.k > 0) {
+    if (some) e.continues = from.s.t0 + from.at.j;
+    // the last worker whose range begins at the token's first tile or ahead of it
+    const long long inner = from.base + cut.tokens(q.vis, from.s, from.at.j) + kTokenCost + kTilePages;
+    e.first = (int)((double)inner * cut.workers / cut.total);
+    if (e.first > w) e.first = w;
+    while (cut.at(e.first) >= inner) --e.first;
+    while (cut.at(e.first + 1) < inner) ++e.first;
   }
-  if (to.k > 0 && !(same && from.k > 0)) e.z = sequence_of(q, to.b).t0 + to.j;
+  if (some && to.at.k > 0 && !(same && from.at.k > 0)) {
+    e.begins = to.s.t0 + to.at.j;
+    // a worker whose range begins at a cost below the token's end holds items of it
+    const long long end = to.base + cut.tokens(q.vis, to.s, to.at.j + 1);
+    e.last = (int)((double)end * cut.workers / cut.total);
+    if (e.last >= cut.workers) e.last = cut.workers - 1;
+    while (e.last + 1 < cut.workers && cut.at(e.last + 1) < end) ++e.last;
+    while (cut.at(e.last) >= end) --e.last;
+  }
   return e;
 }
 

@@ -486,7 +486,7 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
   const chunk::Layout L = chunk::layout(workers);
   char* base = static_cast<char*>(ws);
   const chunk::Params p{b, k->block_table, k->max_blocks_per_seq, k->num_blocks, scale_of(c) * 1.4426950408889634f, g_wait_limit_ns.load(std::memory_order_relaxed), workers,
-                        reinterpret_cast<int4*>(base + L.off_piece), reinterpret_cast<float*>(base + L.off_lse),
+                        1.f / workers, reinterpret_cast<int4*>(base + L.off_shares), reinterpret_cast<float*>(base + L.off_lse),
                         reinterpret_cast<float*>(base + L.off_o), o_lat, lse};
   CUtensorMap m[4];  // queries, their low parts, output, pieces
   MLA_TRY(pairdec::query_map(q, b.n_tok, &m[0]));
@@ -500,8 +500,9 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
   else
     MLA_TRY((split ? chunk_pair_launch<true, chunk::PoolMap>(k, m, p, s)
                    : chunk_pair_launch<false, chunk::PoolMap>(k, m, p, s)));
-  return st(launch_chained(chunk::chunk_merge_kernel, dim3(workers, chunk::kH / chunk::kMergeHeads), dim3(256), 0, s,
-                           workers, (const int4*)p.piece, (const float*)p.part_lse, (const float*)p.part_o, o_lat, lse));
+  return st(launch_chained(chunk::chunk_merge_kernel, dim3(workers, chunk::kH / chunk::kMergeGroups),
+                           dim3(chunk::kMergeThreads), 0, s, (const int4*)p.shares, (const float*)p.part_lse,
+                           (const float*)p.part_o, o_lat, lse));
 }
 
 template <typename TQ, typename T, typename TO>

@@ -18,6 +18,7 @@ ROOT = Path(__file__).resolve().parents[1]
 # first item, end item, items of the token; then its shares; then, per token
 # with items, every item; and the closed-form item sums.
 PROGRAM = r'''
+#include <algorithm>
 #include <cstdio>
 #include <vector>
 #include "chunk_plan.cuh"
@@ -29,19 +30,31 @@ int main() {
     for (auto& x : cu) std::scanf("%d", &x);
     for (auto& x : len) std::scanf("%d", &x);
     const Batch q{cu.data(), len.data(), batch, n_tok, max_rows, Visible{window, sinks}};
+    Cut cut{0, workers, 1.f / workers, 0};
     std::vector<long long> C(batch + 1, 0);
+    long long tokens = 0, longest = 0;
     for (int b = 0; b < batch; ++b) {
       const Sequence s = sequence_of(q, b);
-      C[b + 1] = C[b] + cost_of_tokens(q.vis, s, s.n);
+      cut.total += cut.tokens(q.vis, s, s.n);
+      tokens += s.n;
+      longest = std::max(longest, longest_token(q.vis, s));
     }
-    std::printf("case %lld\n", C[batch]);
+    std::printf("case %lld\n", cut.total);
+    if (one_token_each(tokens, cut.total, longest, workers)) {
+      cut.single = 1;
+      cut.total = tokens;
+    }
+    for (int b = 0; b < batch; ++b) {
+      const Sequence s = sequence_of(q, b);
+      C[b + 1] = C[b] + cut.tokens(q.vis, s, s.n);
+    }
     for (int w = 0; w < workers; ++w) {
-      const Place from = cut(q, C.data(), w, workers), to = cut(q, C.data(), w + 1, workers);
-      for (Walk k(q, from, to); k.valid(); k.next())
+      const Found from = place_at(q, cut, C.data(), cut.at(w)), to = place_at(q, cut, C.data(), cut.at(w + 1));
+      for (Walk k(q, from.at, from.s, to.at); k.valid(); k.next())
         std::printf("piece %d %d %d %d %d %d %d %d\n", w, k.at.b, k.token(), k.position(), k.at.k, k.k1, k.n_items,
                     (int)k.whole());
-      const Shares e = shares_of(q, from, to);
-      std::printf("shares %d %d %d %d\n", w, e.x, e.y, e.z);
+      const Shares e = shares_of(q, cut, from, to, w);
+      std::printf("shares %d %d %d %d %d\n", w, e.continues, e.begins, e.last, e.first);
     }
     for (int b = 0; b < batch; ++b) {
       const Sequence s = sequence_of(q, b);
@@ -148,8 +161,10 @@ def test_pieces_cover_every_visible_row_once(plan):
         for key, (end, parts) in seen.items():
             assert end == (len(items[key]) if want[key] else 0)
             if len(parts) > 1:   # the merge finds them: begun by one, continued and ended by the others
-                assert shares[parts[0][0]][2] == key[1]
-                for w, k0, k1 in parts[1:]:
-                    assert shares[w][0] == key[1] and shares[w][1] == (1 if w == parts[-1][0] else 0)
-        begun = sum(1 for v in shares.values() if v[2] >= 0)
+                head, tail = parts[0][0], parts[-1][0]
+                assert shares[head][1:3] == [key[1], tail]
+                for w in range(head + 1, tail + 1):    # idle workers among them continue nothing
+                    assert shares[w][0] == (key[1] if w in [q[0] for q in parts] else -1)
+                    assert shares[w][3] == head
+        begun = sum(1 for v in shares.values() if v[1] >= 0)
         assert begun == sum(1 for _, parts in seen.values() if len(parts) > 1)
