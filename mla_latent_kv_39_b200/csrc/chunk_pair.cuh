@@ -497,7 +497,23 @@ struct Issuer {
       ph ^= 1;
     }
   }
-  __device__ bool scores(int i, bool first, bool last) {
+  // what the MMAs need of a tile's record
+  struct Next {
+    int n;
+    bool first, last;
+  };
+  __device__ bool look(int i, Next& t) {
+    if (!wait_tile(sm, i, wns)) return false;
+    const Tile& r = sm.tile[i % kTiles];
+    t.n = uni(r.n);
+    t.first = uni(r.first);
+    t.last = uni(r.last);
+    release_tile(sm, i, one);
+    return true;
+  }
+  // The scores of tile i; on the way, with MMAs in the pipe, the record of the
+  // tile behind it is read.
+  __device__ bool scores(int i, bool first, bool last, Next& ahead) {
     if (first && !warp_wait(&sm.q_full, nq++ & 1, 50, wns)) return false;
     const uint32_t d = tmem + kTmemS + 128 * (i & 1);
 #pragma unroll
@@ -520,6 +536,7 @@ struct Issuer {
         }
       }
       __syncwarp();
+      if (e == kSlabs / 2 && !look(i + 1, ahead)) return false;
     }
     return true;
   }
@@ -553,19 +570,14 @@ struct Issuer {
 template <bool kSplit>
 __device__ void mma_role(Smem<kSplit>& sm, uint32_t tmem, const Params& p) {
   Issuer<kSplit> is(sm, tmem, p.wait_ns);
+  typename Issuer<kSplit>::Next t, ahead;
   int i = 0, n_prev = 0;
-  bool ok = true, first_prev = false;
-  for (;; ++i) {
-    ok = ok && wait_tile(sm, i, p.wait_ns);
-    if (!ok) break;
-    const Tile& t = sm.tile[i % kTiles];
-    const int n = uni(t.n);
-    const bool first = uni(t.first), last = uni(t.last);
-    if (n == 0) break;
-    release_tile(sm, i, is.one);
-    ok = is.scores(i, first, last) && (i == 0 || is.values(i - 1, n_prev, first_prev));
-    n_prev = n;
-    first_prev = first;
+  bool first_prev = false, ok = is.look(0, t);
+  for (; ok && t.n > 0; ++i) {
+    ok = is.scores(i, t.first, t.last, ahead) && (i == 0 || is.values(i - 1, n_prev, first_prev));
+    n_prev = t.n;
+    first_prev = t.first;
+    t = ahead;
   }
   if (ok && i > 0) ok = is.values(i - 1, n_prev, first_prev);
   if (!ok) set_abort(sm);
