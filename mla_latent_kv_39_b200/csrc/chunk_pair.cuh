@@ -643,7 +643,12 @@ struct Softmax {
   // whole token's in bf16 to o_lat, 64 columns a pass, a part's in fp32 to the
   // workspace, 32 columns a pass.  Plain stores, a row to a lane, kept the warps
   // 2.8 us a token; here the tensor pipe computes the next tile's scores meanwhile.
+  __device__ void own_free() {  // the bulk stores have read what was there
+    if (one) bulk_wait_read_all();
+    __syncwarp();
+  }
   __device__ void put(uint8_t* own, const uint32_t (&v)[32], const CUtensorMap* map, int x, int y) {
+    own_free();
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       *reinterpret_cast<uint4*>(own + lane * 128 + ((c ^ (lane & 7)) << 4)) =
@@ -653,7 +658,6 @@ struct Softmax {
     if (one) {
       tma_store_2d(map, own, x, y);
       bulk_commit_group();
-      bulk_wait_read_all();
     }
     __syncwarp();
   }
@@ -794,6 +798,7 @@ struct Softmax {
       if (close) {
         write_out(own, open);
         store_lse(open);
+        own_free();
       }
       // row l mod 64 of the item's P slab, K-major with the 128-byte swizzle
       if (q < n) {

@@ -13,7 +13,7 @@
 // start of the window is two items.  Page order does not matter to a softmax.
 //
 // The number of items of a token is a sum of floors of its position, so the
-// items of a whole run of tokens have a closed form, and the cut of all work
+// cost of a whole run of tokens has a closed form, and the cut of all work
 // into equal parts needs one prefix sum over the sequences, not over the
 // tokens: a warp of every CTA makes it for itself (8 bytes read per sequence) and
 // there is no planning launch ahead of the attention.
@@ -27,12 +27,13 @@ namespace chunk {
 constexpr int kPage = 64;
 constexpr int kMaxBatch = 8192;   // sequences of a call: their prefix sums sit in shared memory
 constexpr int kTilePages = 4;     // items of a tile of the tensor-core kernel
-// A token's fixed cost in items: its query load and epilogue, and the unused
-// part of its last tile.
-constexpr int kTokenCost = 3;
-// What cutting tokens into pieces costs the call, in items of one worker: pieces
-// written to the workspace and joined by another kernel (about 10 us, a tile 2.4).
-constexpr int kSplitCost = 16;
+// Costs, in eighths of a full tile's time.  A tile takes its score MMAs whatever
+// its items (half of a full tile's time, 4) and its value MMAs and loads by the
+// item (1 each); a token on top of its tiles the change of queries and output.
+constexpr int kTileCost = 4, kFullTile = kTileCost + kTilePages, kTokenCost = 4;
+// What cutting tokens into pieces costs the call on top: pieces written to the
+// workspace and joined by another kernel (about 10 us, a tile 2.5).
+constexpr int kSplitCost = 4 * kFullTile;
 
 struct Visible {
   int window, sinks;  // window = 0: all rows up to the token's own
@@ -48,23 +49,35 @@ struct Visible {
     const int w0 = start(p);
     return (w0 > 0 ? sink_items() : 0) + p / kPage - w0 / kPage + 1;
   }
-  // sum over p < n of floor(p / 64)
-  __host__ __device__ static long long floors(long long n) {
-    const long long q = n / kPage, r = n % kPage;
-    return kPage * (q * (q - 1) / 2) + q * r;
+  __host__ __device__ int tiles(int p) const { return (items(p) + kTilePages - 1) / kTilePages; }
+  __host__ __device__ int cost(int p) const { return kTileCost * tiles(p) + items(p); }
+  // sum over p < n of floor(p / step)
+  __host__ __device__ static long long floors(long long n, int step) {
+    const long long q = n / step, r = n % step;
+    return step * (q * (q - 1) / 2) + q * r;
   }
-  // items of the tokens at positions p0 .. p0 + n - 1
-  __host__ __device__ long long items_of_run(long long p0, long long n) const {
-    long long s = n + floors(p0 + n) - floors(p0);
-    if (window > 0) {
-      const long long lone = (long long)sinks + window;  // first position whose window is apart from the sinks
-      const long long f = p0 > lone ? p0 : lone;
-      if (f < p0 + n) {
-        const long long m = p0 + n - f;
-        s += m * sink_items() - (floors(p0 + n - window + 1) - floors(f - window + 1));
-      }
+  // Cost of the tokens at positions p0 .. p0 + n - 1.  Up to position sinks +
+  // window - 1 a token sees one run from row 0: p / 64 + 1 items, p / 256 + 1
+  // tiles.  Behind it the sink items and, with window - 1 = 64 a + c, a + 1 items
+  // of the window, one more where p mod 64 < c.
+  __host__ __device__ long long cost_of_run(long long p0, long long n) const {
+    const long long end = p0 + n, apart = window == 0 ? end : (long long)sinks + window;
+    const long long m = apart < p0 ? p0 : (apart < end ? apart : end);  // [p0, m): one run; [m, end): apart
+    constexpr int kRun = kPage * kTilePages;
+    long long s = (m - p0) * (kTileCost + 1) + kTileCost * (floors(m, kRun) - floors(p0, kRun)) + floors(m, kPage) -
+                  floors(p0, kPage);
+    if (m < end) {
+      const int c = (window - 1) % kPage, few = sink_items() + (window - 1) / kPage + 1;
+      const long long more = past(end, c) - past(m, c);  // tokens with one item more
+      s += (end - m) * (kTileCost * ((few + kTilePages - 1) / kTilePages) + few) + more;
+      if (few % kTilePages == 0) s += kTileCost * more;
     }
     return s;
+  }
+  // how many p < n have p mod 64 < c
+  __host__ __device__ static long long past(long long n, int c) {
+    const long long r = n % kPage;
+    return n / kPage * c + (r < c ? r : c);
   }
 };
 
@@ -138,7 +151,7 @@ struct Cut {
   float inv;        // 1 / workers
   int single;
   __host__ __device__ long long tokens(const Visible& vis, const Sequence& s, int n) const {
-    return single ? n : (long long)kTokenCost * n + (s.p0 >= 0 ? vis.items_of_run(s.p0, n) : 0);
+    return single ? n : (long long)kTokenCost * n + (s.p0 >= 0 ? vis.cost_of_run(s.p0, n) : 0);
   }
   // The cost where the range of worker w begins (w = workers: where the last
   // ends): growing in w, and the same for the worker that ends there.
@@ -153,7 +166,7 @@ __host__ __device__ inline bool one_token_each(long long tokens, long long total
 }
 // The longest cost that a token of the sequence may have.
 __host__ __device__ inline long long longest_token(const Visible& vis, const Sequence& s) {
-  return s.n > 0 && s.p0 >= 0 ? kTokenCost + vis.items(s.p0 + s.n - 1) + 1 : 0;
+  return s.n > 0 && s.p0 >= 0 ? kTokenCost + vis.cost(s.p0 + s.n - 1) + kTileCost : 0;
 }
 
 // A place in the order of all items: sequence, token within it, item.
@@ -190,9 +203,9 @@ __host__ __device__ inline Found place_at(const Batch& q, const Cut& cut, const 
   }
   int k = 0;
   if (f.s.p0 >= 0 && !cut.single) {
-    const long long i = r - cut.tokens(q.vis, f.s, a) - kTokenCost;
-    const int n = q.vis.items(f.s.p0 + a);
-    k = i <= 0 ? 0 : (int)(i < n ? i : n - 1) / kTilePages * kTilePages;
+    const long long i = (r - cut.tokens(q.vis, f.s, a) - kTokenCost) / kFullTile;  // rounds towards 0
+    const int n = q.vis.tiles(f.s.p0 + a);
+    k = (i < n ? (int)i : n - 1) * kTilePages;
   }
   f.at = {lo, a, k};
   return f;
@@ -264,7 +277,7 @@ __host__ __device__ inline Shares shares_of(const Batch& q, const Cut& cut, cons
   if (from.at.k > 0) {
     if (some) e.continues = from.s.t0 + from.at.j;
     // the last worker whose range begins at the token's first tile or ahead of it
-    const long long inner = from.base + cut.tokens(q.vis, from.s, from.at.j) + kTokenCost + kTilePages;
+    const long long inner = from.base + cut.tokens(q.vis, from.s, from.at.j) + kTokenCost + kFullTile;
     e.first = (int)((double)inner * cut.workers / cut.total);
     if (e.first > w) e.first = w;
     while (cut.at(e.first) >= inner) --e.first;

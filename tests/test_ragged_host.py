@@ -146,7 +146,7 @@ def test_pieces_cover_every_visible_row_once(plan):
             assert all(0 <= a < e <= 64 for _, a, e in its)
             if window == 0 or window >= 64:        # a range cut on both sides needs a window shorter than a page
                 assert all(a == 0 or e == 64 for _, a, e in its)
-            cost += 3 + len(its)
+            cost += 4 + 4 * -(-len(its) // 4) + len(its)
         assert cost == total
         # every token's items exactly once, in order over the workers; cuts on tile boundaries
         seen = {}
