@@ -144,6 +144,7 @@ struct Params {
   unsigned long long wait_ns;
   int workers;
   float inv_workers;
+  int single;       // a token to a worker, whatever the costs (then no merge follows)
   int4* shares;     // the workers' Shares
   float* part_lse;
   float* part_o;
@@ -250,7 +251,7 @@ __device__ __forceinline__ Cut find_range(const Params& p, long long* C, int wor
   cut.total = shfl64(x, 31);
   long long ahead = x - mine;
   const long long tokens = shfl64(t, 31);
-  if (one_token_each(tokens, cut.total, longest, p.workers)) {
+  if (p.single || one_token_each(tokens, cut.total, longest, p.workers)) {
     cut.single = 1;
     cut.total = tokens;
     ahead = t - own;
@@ -911,29 +912,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Joins the pieces of the tokens that several workers share:
 //   o_lat = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).
 // Grid (workers, heads / 4).  A token of few pieces is joined by the blocks of
-// the worker that begins it, four heads to a block, one to each group of 64
-// threads.  Of a token of many pieces (a long request) the blocks of its first
-// four workers take a head each, its pieces dealt to the four groups: 128 blocks
-// that read 150 KB each of 74 pieces, against 32 with 600 KB.  A thread owns 8
-// latent columns; several loads are in flight, under no condition.  An idle
-// worker's place counts as a piece without visible rows (lse -inf).  Sums run in
-// a fixed order.
-constexpr int kMergeThreads = 256, kMergeGroups = kMergeThreads / 64, kMergeFew = 8;
+// the worker that begins it, four heads to a block, one to each 64 threads.  Of a
+// token of many pieces (a long request) the blocks of its first eight workers
+// take half a head each, the pieces dealt to the eight warps: 256 blocks that
+// read 75 KB each of 74 pieces (28 us by 32 blocks of whole heads, 13 us by 128 of
+// one head).  A thread owns 8 latent columns; three loads are in flight, under no
+// condition.  An idle worker's place counts as a piece without visible rows (lse
+// -inf).  Sums run in a fixed order.
+constexpr int kMergeThreads = 256, kMergeHeads = 4, kMergeFew = 8;
 
 __global__ void __launch_bounds__(kMergeThreads, 6) chunk_merge_kernel(const int4* __restrict__ shares,
-                                                                    const float* __restrict__ part_lse,
-                                                                    const float* __restrict__ part_o,
-                                                                    bf16* __restrict__ o_lat,
-                                                                    float* __restrict__ lse_out) {
+                                                                       const float* __restrict__ part_lse,
+                                                                       const float* __restrict__ part_o,
+                                                                       bf16* __restrict__ o_lat,
+                                                                       float* __restrict__ lse_out) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float wt[kMergeGroups][kMaxWorkers];
-  __shared__ float4 sum[kMergeGroups][2][64];
+  __shared__ float wt[kMaxWorkers + kMergeHeads * kMergeFew];  // weights: one list of many, or four of few
+  __shared__ float4 sum[kMergeThreads / 32][2][32];
   const int w = blockIdx.x;
   int4 own = shares[w];
   int w0 = w;
   if (own.y < 0 || own.z - w0 < kMergeFew) {  // not the first worker of a token of many pieces: one of its next?
-    if (own.w >= 0 && w - own.w < kMergeGroups) {
+    if (own.w >= 0 && w - own.w < kMergeFew) {
       const int4 head = shares[own.w];
       if (head.z - own.w >= kMergeFew) {
         w0 = own.w;
@@ -944,43 +945,45 @@ __global__ void __launch_bounds__(kMergeThreads, 6) chunk_merge_kernel(const int
   const int tok = own.y, n = own.z - w0 + 1;
   if (tok < 0) return;
   const bool many = n > kMergeFew;
-  const int group = threadIdx.x / 64, col = threadIdx.x % 64, lane = threadIdx.x & 31;
-  const int h = kMergeGroups * blockIdx.y + (many ? w - w0 : group);
-  const int list = many ? 0 : group;  // of many, one list of weights for all groups
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int h = kMergeHeads * blockIdx.y + (many ? (w - w0) / 2 : warp / 2);
+  const int d = many ? kDc / 2 * ((w - w0) & 1) + 8 * lane : 8 * (threadIdx.x % 64);
+  float* list = many ? wt : wt + kMergeFew * (warp / 2);
   // piece i: the beginning with worker w0, the rest with the workers behind it
   const auto slot_of = [&](int i) { return 2 * (w0 + i) + (i == 0 ? 1 : 0); };
-  if (col < 32 && (!many || group == 0)) {
+  if (many ? warp == 0 : warp % 2 == 0) {
     float M = -INFINITY, Z = 0.f;
     for (int i = lane; i < n; i += 32) {
       const float x = part_lse[(long long)slot_of(i) * kH + h];
-      wt[list][i] = x;
+      list[i] = x;
       M = fmaxf(M, x);
       if (x != x) Z = x;  // the maximum passes over NaN, the sum must not
     }
     M = warp_max(M);
     for (int i = lane; i < n; i += 32) {
-      const float x = M == -INFINITY ? 0.f : exp2f(wt[list][i] - M);  // M = -inf: no piece has a visible row
-      wt[list][i] = x;
+      const float x = M == -INFINITY ? 0.f : exp2f(list[i] - M);  // M = -inf: no piece has a visible row
+      list[i] = x;
       Z += x;
     }
     Z = warp_sum(Z);
     const float inv = Z == 0.f ? 0.f : 1.f / Z;
-    for (int i = lane; i < n; i += 32) wt[list][i] *= inv;
-    if (lse_out != nullptr && lane == 0) lse_out[(long long)tok * kH + h] = Z == 0.f ? -INFINITY : M + log2f(Z);
+    for (int i = lane; i < n; i += 32) list[i] *= inv;
+    if (lse_out != nullptr && lane == 0 && d < kDc / 2)
+      lse_out[(long long)tok * kH + h] = Z == 0.f ? -INFINITY : M + log2f(Z);
   }
   __syncthreads();
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const auto add = [&](int i, const float4& x, const float4& y) {
-    const float f = i < n ? wt[list][i] : 0.f;
+    const float f = i < n ? list[i] : 0.f;
     const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = fmaf(f, f == 0.f ? 0.f : v[c], acc[c]);  // weight 0: nothing was written there
   };
   const auto at = [&](int i) {
-    return reinterpret_cast<const float4*>(part_o + ((long long)slot_of(min(i, n - 1)) * kH + h) * kDc + 8 * col);
+    return reinterpret_cast<const float4*>(part_o + ((long long)slot_of(min(i, n - 1)) * kH + h) * kDc + d);
   };
-  const int step = many ? kMergeGroups : 1;
-  for (int i = many ? group : 0; i < n; i += 3 * step) {
+  const int step = many ? kMergeThreads / 32 : 1;
+  for (int i = many ? warp : 0; i < n; i += 3 * step) {
     const float4 x0 = __ldcs(at(i)), y0 = __ldcs(at(i) + 1);
     const float4 x1 = __ldcs(at(i + step)), y1 = __ldcs(at(i + step) + 1);
     if (n > 2) {
@@ -994,22 +997,22 @@ __global__ void __launch_bounds__(kMergeThreads, 6) chunk_merge_kernel(const int
     }
   }
   if (many) {
-    sum[group][0][col] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    sum[group][1][col] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    sum[warp][0][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    sum[warp][1][lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
     __syncthreads();
-    if (group > 0) return;
+    if (warp > 0) return;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int g = 1; g < kMergeGroups; ++g) {
-        const float4 v = sum[g][e][col];
+      for (int g = 1; g < kMergeThreads / 32; ++g) {
+        const float4 v = sum[g][e][lane];
         acc[4 * e] += v.x;
         acc[4 * e + 1] += v.y;
         acc[4 * e + 2] += v.z;
         acc[4 * e + 3] += v.w;
       }
   }
-  *reinterpret_cast<uint4*>(o_lat + ((long long)tok * kH + h) * kDc + 8 * col) =
+  *reinterpret_cast<uint4*>(o_lat + ((long long)tok * kH + h) * kDc + d) =
       make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
                  pack_bf16x2(acc[6], acc[7]));
 }

@@ -51,6 +51,12 @@ struct Visible {
   }
   __host__ __device__ int tiles(int p) const { return (items(p) + kTilePages - 1) / kTilePages; }
   __host__ __device__ int cost(int p) const { return kTileCost * tiles(p) + items(p); }
+  // the most that a token may cost in sequences of up to `rows` rows
+  __host__ __device__ long long most_cost(int rows) const {
+    const long long all = rows / kPage + 1, some = (long long)sink_items() + window / kPage + 2;
+    const long long n = window > 0 && some < all ? some : all;
+    return kTokenCost + kTileCost * (n / kTilePages + 1) + n;
+  }
   // sum over p < n of floor(p / step)
   __host__ __device__ static long long floors(long long n, int step) {
     const long long q = n / step, r = n % step;
@@ -166,7 +172,7 @@ __host__ __device__ inline bool one_token_each(long long tokens, long long total
 }
 // The longest cost that a token of the sequence may have.
 __host__ __device__ inline long long longest_token(const Visible& vis, const Sequence& s) {
-  return s.n > 0 && s.p0 >= 0 ? kTokenCost + vis.cost(s.p0 + s.n - 1) + kTileCost : 0;
+  return s.n > 0 && s.p0 >= 0 ? kTokenCost + vis.cost(s.p0 + s.n - 1) : 0;
 }
 
 // A place in the order of all items: sequence, token within it, item.

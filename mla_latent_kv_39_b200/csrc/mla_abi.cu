@@ -484,9 +484,13 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
                          bf16* o_lat, float* lse, void* ws, cudaStream_t s) {
   const bool split = (c->flags & MLA_FLAG_SPLIT_QUERY) != 0;
   const chunk::Layout L = chunk::layout(workers);
+  // Few short tokens: the table's width alone says that each has a worker and
+  // none is split (the kernel comes to the same), so there is nothing to merge.
+  const bool whole = b.n_tok <= workers && b.vis.most_cost(b.max_rows) <= chunk::kSplitCost;
+  if (whole) workers = b.n_tok;
   char* base = static_cast<char*>(ws);
   const chunk::Params p{b, k->block_table, k->max_blocks_per_seq, k->num_blocks, scale_of(c) * 1.4426950408889634f, g_wait_limit_ns.load(std::memory_order_relaxed), workers,
-                        1.f / workers, reinterpret_cast<int4*>(base + L.off_shares), reinterpret_cast<float*>(base + L.off_lse),
+                        1.f / workers, whole ? 1 : 0, reinterpret_cast<int4*>(base + L.off_shares), reinterpret_cast<float*>(base + L.off_lse),
                         reinterpret_cast<float*>(base + L.off_o), o_lat, lse};
   CUtensorMap m[4];  // queries, their low parts, output, pieces
   MLA_TRY(pairdec::query_map(q, b.n_tok, &m[0]));
@@ -500,7 +504,8 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
   else
     MLA_TRY((split ? chunk_pair_launch<true, chunk::PoolMap>(k, m, p, s)
                    : chunk_pair_launch<false, chunk::PoolMap>(k, m, p, s)));
-  return st(launch_chained(chunk::chunk_merge_kernel, dim3(workers, chunk::kH / chunk::kMergeGroups),
+  if (whole) return MLA_OK;
+  return st(launch_chained(chunk::chunk_merge_kernel, dim3(workers, chunk::kH / chunk::kMergeHeads),
                            dim3(chunk::kMergeThreads), 0, s, (const int4*)p.shares, (const float*)p.part_lse,
                            (const float*)p.part_o, o_lat, lse));
 }
