@@ -2,7 +2,9 @@
 
 ``abi`` wraps the five C entry points of ``libmla.so`` (cache append, query
 absorption, split-KV decode, split combine, output projection) one to one;
-``layer.DecodeLayer`` sequences them for one layer's decode step.
+``layer.DecodeLayer`` sequences them for one layer's decode step, and
+``layer.RaggedLayer`` for a batch whose requests bring different numbers of
+new tokens (request tables, slots, chunk or window attention).
 """
 
 from .abi import (  # noqa: F401
@@ -42,5 +44,5 @@ from .abi import (  # noqa: F401
     mla_query_packed_bytes,
     mla_window_attention,
 )
-from .layer import DecodeLayer  # noqa: F401
+from .layer import DecodeLayer, RaggedLayer  # noqa: F401
 from .shard import ShardPlan, decode_shard, decode_sharded, gather_partials, shard_plan  # noqa: F401

@@ -162,6 +162,13 @@ class Config:
         return torch.uint8 if self.fp8_cache else self.torch_dtype
 
     def c(self) -> MLAConfig:
+        c = self.__dict__.get("_c")      # made once: every call passes it
+        if c is None:
+            c = self._make_c()
+            object.__setattr__(self, "_c", c)
+        return c
+
+    def _make_c(self) -> MLAConfig:
         return MLAConfig(self.hidden, self.n_heads, self.d_c, self.d_r, self.qk_nope, self.v_head,
                          self.q_lora, self.rope_theta, self.softmax_scale, self.block_size,
                          MLA_BF16 if self.dtype == "bf16" else MLA_F32,
@@ -185,6 +192,9 @@ class Cache:
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, ndim=None, shape=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype == dtype)
+            and (ndim is None or t.dim() == ndim) and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -204,8 +214,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the raw handle: making a Stream object took 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -439,12 +449,12 @@ def mla_out_proj(cfg: Config, o_lat, W_UV, W_O, y, workspace, stream=None):
 
 # --------------------------------------------------------------- ragged steps
 
-def _need_here(**tensors):
+def _need_here(*tensors):
     """Every given tensor is on the current device (the library launches there)."""
     here = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != here:
-            raise ValueError(f"{name} must be on the current device cuda:{here}, got {t.device}")
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"every tensor must be on the current device cuda:{here}, got one on {t.device}")
 
 
 def mla_batch_tables(cfg: Config, cached_lens, new_lens, free_blocks, free_head, num_blocks: int, block_table, cu_q,
@@ -470,7 +480,7 @@ def mla_batch_tables(cfg: Config, cached_lens, new_lens, free_blocks, free_head,
     _need(seq_idx, "seq_idx", i32, shape=(n_tok,))
     _need(pos, "pos", i32, shape=(n_tok,))
     _need(slots, "slots", torch.int64, shape=(n_tok,))
-    _need_here(cached_lens=cached_lens, new_lens=new_lens, free_blocks=free_blocks, block_table=block_table, pos=pos)
+    _need_here(cached_lens, new_lens, free_blocks, free_head, block_table, cu_q, seq_lens, seq_idx, pos, slots, free_head_out)
     _check(lib().mla_batch_tables(ctypes.byref(cfg.c()), batch, _ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks),
                                   free_blocks.shape[0], _ptr(free_head), num_blocks, _ptr(block_table),
                                   block_table.shape[1], n_tok, _ptr(cu_q), _ptr(seq_lens), _ptr(seq_idx), _ptr(pos),
@@ -489,7 +499,7 @@ def mla_cache_append_slots(cfg: Config, x, W_DKV, W_KR, pos, slots, cache: Cache
     _need(workspace, "workspace", torch.uint8)
     if cache.pool.dtype != cfg.cache_torch_dtype or cache.pool.shape[1:] != (cfg.block_size, cfg.d_c + cfg.d_r):
         raise ValueError("cache pool dtype/shape does not match the config")
-    _need_here(x=x, slots=slots, pool=cache.pool, workspace=workspace)
+    _need_here(x, W_DKV, W_KR, pos, slots, cache.pool, workspace)
     _check(lib().mla_cache_append_slots(ctypes.byref(cfg.c()), _ptr(x), n, _ptr(W_DKV), _ptr(W_KR), _ptr(pos),
                                         _ptr(slots), ctypes.byref(cache.c), _ptr(workspace), workspace.numel(),
                                         _stream(stream)), "mla_cache_append_slots")
@@ -522,7 +532,7 @@ def _chunk_args(cfg: Config, q, cu_q, cache: Cache, seq_lens, o_lat, workspace, 
     _need(workspace, "workspace", torch.uint8)
     if cache.pool.dtype != cfg.cache_torch_dtype or cache.pool.shape[1:] != (cfg.block_size, cfg.d_c + cfg.d_r):
         raise ValueError("cache pool dtype/shape does not match the config")
-    _need_here(q=q_lat, cu_q=cu_q, seq_lens=seq_lens, pool=cache.pool, o_lat=o_lat, lse=lse, workspace=workspace)
+    _need_here(q_lat, cu_q, seq_lens, cache.pool, o_lat, lse, workspace)
     return n, batch, q_lat, q_rope
 
 

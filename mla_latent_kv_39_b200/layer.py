@@ -259,3 +259,107 @@ class DecodeLayer:
             y = self.step(x, seq_idx, pos, seq_lens, stream)
             y_host.copy_(y, non_blocking=True)
         return y_host
+
+
+class RaggedLayer:
+    """One MLA layer's step for a batch whose requests bring different numbers
+    of new tokens: none, one (a decode) or a prompt's chunk.
+
+    All new tokens lie one behind the other in ``x`` ``[n_tok, hidden]``, request
+    by request; rows behind the last token are padding (``n_tok`` is the largest
+    step's), so that one captured graph serves every step.  A step builds the
+    tables on the device (``mla_batch_tables``: pages for the new tokens come
+    from ``free_blocks``), projects the queries, stores the new latent rows
+    through their slots, attends (causally, or over a sliding window and a few
+    first rows) and projects the output.  ``cache.block_table`` is extended in
+    place.  ``window`` = 0: all rows up to the token's own."""
+
+    def __init__(self, cfg: abi.Config, weights: Dict[str, torch.Tensor], cache: abi.Cache, n_tok: int,
+                 window: int = 0, n_sinks: int = 0, max_workers: int = 0):
+        if window < 0 or n_sinks < 0:
+            raise ValueError("window and n_sinks must not be negative")
+        self.cfg, self.W, self.cache, self.n_tok = cfg, weights, cache, n_tok
+        self.window, self.n_sinks, self.max_workers = window, n_sinks, max_workers
+        dev, H = cache.pool.device, cfg.n_heads
+        batch, width = cache.block_table.shape
+        # an FP8 cache is expanded into a bf16 scratch for the step, as in DecodeLayer
+        self.dcfg, self.dcache, self.fp8_scratch = cfg, cache, None
+        if cfg.fp8_cache:
+            import dataclasses
+            self.dcfg = dataclasses.replace(cfg, fp8_cache=False)
+            self.fp8_scratch = torch.empty(abi.mla_fp8_scratch_bytes(cfg, batch, width), dtype=torch.uint8, device=dev)
+            self.dcache = abi.fp8_scratch_cache(self.dcfg, self.fp8_scratch, batch, width)
+        cfg = self.dcfg
+        if cfg.dtype == "bf16":
+            self.q = torch.empty((2 if cfg.split_query else 1) * n_tok, H, cfg.d_c + cfg.d_r, dtype=torch.bfloat16, device=dev)
+        else:
+            self.q = (torch.empty(n_tok, H, cfg.d_c, device=dev), torch.empty(n_tok, H, cfg.d_r, device=dev))
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.cu_q = torch.zeros(batch + 1, **i32)
+        self.seq_lens = torch.zeros(batch, **i32)
+        self.seq_idx = torch.zeros(n_tok, **i32)
+        self.pos = torch.zeros(n_tok, **i32)
+        self.slots = torch.zeros(n_tok, dtype=torch.int64, device=dev)
+        # padding rows are never written: zeros, so that their projections stay finite
+        self.o_lat = torch.zeros(n_tok, H, cfg.d_c, dtype=cfg.torch_dtype, device=dev)
+        self.lse = torch.zeros(n_tok, H, device=dev)
+        self.y = torch.empty(n_tok, cfg.hidden, dtype=cfg.torch_dtype, device=dev)
+        u8 = dict(dtype=torch.uint8, device=dev)
+        self.ws_gemm = torch.empty(max(abi.mla_absorb_q_workspace_size(cfg, n_tok), abi.mla_out_proj_workspace_size(cfg, n_tok),
+                                       256), **u8)
+        self.ws_append = torch.empty(max(abi.mla_cache_append_workspace_size(cfg, n_tok), 256), **u8)
+        self.ws_attend = torch.empty(abi.mla_chunk_workspace_size(cfg, n_tok, max_workers), **u8)
+        self.side = torch.cuda.Stream(device=dev)
+
+    def tables(self, cached_lens, new_lens, free_blocks, free_head, stream=None):
+        """Tables, positions and slots of a step; ``self.seq_lens`` afterwards holds the next step's ``cached_lens``."""
+        abi.mla_batch_tables(self.cfg, cached_lens, new_lens, free_blocks, free_head, self.cache.pool.shape[0],
+                             self.cache.block_table, self.cu_q, self.seq_lens, self.seq_idx, self.pos, self.slots,
+                             stream=stream)
+
+    def attend(self, stream=None):
+        """Attention of the step's tokens: ``self.o_lat`` (storage dtype) and ``self.lse``."""
+        if self.fp8_scratch is not None:
+            abi.mla_cache_dequant_fp8(self.cfg, self.cache, self.seq_lens.shape[0], self.seq_lens, self.fp8_scratch, stream)
+        args = (self.o_lat, self.ws_attend, self.lse, self.max_workers, stream)
+        if self.window:
+            abi.mla_window_attention(self.dcfg, self.q, self.cu_q, self.dcache, self.seq_lens, self.window, self.n_sinks, *args)
+        else:
+            abi.mla_chunk_attention(self.dcfg, self.q, self.cu_q, self.dcache, self.seq_lens, *args)
+
+    def step(self, x, cached_lens, new_lens, free_blocks, free_head, stream=None) -> torch.Tensor:
+        """One step on device tensors: ``y`` ``[n_tok, hidden]`` (a reused buffer; padding rows mean nothing).
+        ``free_head`` moves on in place; pass ``self.seq_lens`` as the next step's ``cached_lens``."""
+        main = stream or torch.cuda.current_stream()
+        self.tables(cached_lens, new_lens, free_blocks, free_head, main)
+        ready = torch.cuda.Event()
+        ready.record(main)
+        W, cfg = self.W, self.dcfg
+        W_UQ = W["W_UQ"] if "W_UQ" in W else W["W_Q"]
+        if cfg.dtype == "bf16":
+            abi.mla_absorb_q_packed(cfg, x, W.get("W_DQ"), W_UQ, W["W_UK"], self.pos, self.q, self.ws_gemm, main)
+        else:
+            abi.mla_absorb_q(cfg, x, W.get("W_DQ"), W_UQ, W["W_UK"], self.pos, *self.q, self.ws_gemm, main)
+        # the new rows on a second stream beside the query projections
+        self.side.wait_event(ready)
+        abi.mla_cache_append_slots(self.cfg, x, W["W_DKV"], W["W_KR"], self.pos, self.slots, self.cache, self.ws_append,
+                                   self.side)
+        done = torch.cuda.Event()
+        done.record(self.side)
+        main.wait_event(done)
+        x.record_stream(self.side)
+        self.attend(main)
+        abi.mla_out_proj_stored(cfg, self.o_lat, W["W_UV"], W["W_O"], self.y, self.ws_gemm, main)
+        return self.y
+
+    def capture_step(self, x, cached_lens, new_lens, free_blocks, free_head) -> torch.cuda.CUDAGraph:
+        """Record one ``step`` on these device buffers as a CUDA graph.  Refill ``x``, ``cached_lens`` and
+        ``new_lens`` in place between replays (``free_head`` moves on by itself); ``self.y`` holds the result.
+        The kernels' one-time setup is done first by a step without new tokens, which changes nothing."""
+        none = torch.zeros_like(new_lens)
+        self.step(x, cached_lens, none, free_blocks, free_head)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            self.step(x, cached_lens, new_lens, free_blocks, free_head)
+        return graph
