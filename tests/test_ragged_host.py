@@ -168,3 +168,92 @@ def test_pieces_cover_every_visible_row_once(plan):
                     assert shares[w][3] == head
         begun = sum(1 for v in shares.values() if v[1] >= 0)
         assert begun == sum(1 for _, parts in seen.values() if len(parts) > 1)
+
+
+# ---------------------------------------------------------------- refusals, before any launch
+
+V3 = dict(hidden=7168, n_heads=128, d_c=512, d_r=64, qk_nope=128, v_head=128, q_lora=1536)
+OK, ODD = 1 << 20, (1 << 20) + 8          # never dereferenced: every call below is refused
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return abi.load_library()
+
+
+def _cfg(**kw):
+    return abi.Config(**{**V3, "dtype": "bf16", **kw}).c()
+
+
+def chunk(lib, cfg, window=None, **kw):
+    a = dict(q=OK, q_rope=None, n_tok=4, cu_q=OK, batch=2, cache=abi.MLACache(OK, 8, OK, 2, 3), seq_lens=OK, workers=0,
+             o_lat=OK, lse=OK, ws=OK, ws_bytes=1 << 40)
+    a.update(kw)
+    head = (ctypes.byref(cfg), a["q"], a["q_rope"], a["n_tok"], a["cu_q"], a["batch"], ctypes.byref(a["cache"]), a["seq_lens"])
+    tail = (a["workers"], a["o_lat"], a["lse"], a["ws"], a["ws_bytes"], None)
+    return lib.mla_chunk_attention(*head, *tail) if window is None else lib.mla_window_attention(*head, *window, *tail)
+
+
+@pytest.mark.parametrize("window", [None, (64, 4)])
+def test_attention_refuses_bad_arguments(lib, window):
+    bf = _cfg()
+    bad = abi.MLA_ERR_INVALID_ARG
+    for kw in (dict(n_tok=-1), dict(batch=-1), dict(workers=-1), dict(q=None), dict(cu_q=None), dict(seq_lens=None),
+               dict(o_lat=None), dict(ws=None), dict(q=ODD), dict(o_lat=ODD), dict(ws=ODD), dict(lse=OK + 2), dict(cu_q=OK + 1),
+               dict(cache=abi.MLACache(ODD, 8, OK, 2, 3)), dict(cache=abi.MLACache(OK, 8, OK, 1, 3)),
+               dict(cache=abi.MLACache(OK, 0, OK, 2, 3)), dict(q_rope=OK)):
+        assert chunk(lib, bf, window, **kw) == bad, kw
+    for kw in (dict(q_rope=None), dict(q_rope=OK, q=OK + 2), dict(q_rope=OK + 2)):     # fp32 storage takes two arrays
+        assert chunk(lib, _cfg(dtype="f32"), window, **kw) == bad, kw
+    assert chunk(lib, _cfg(fp8_cache=True), window, q_rope=OK) == bad                   # no row scales
+    assert chunk(lib, bf, window, batch=9000, cache=abi.MLACache(OK, 8, OK, 9000, 3)) == abi.MLA_ERR_UNSUPPORTED
+    assert chunk(lib, bf, window, n_tok=1 << 25) == abi.MLA_ERR_UNSUPPORTED
+    assert chunk(lib, _cfg(d_c=1024), window) == abi.MLA_ERR_UNSUPPORTED                # rows past the CUDA-core kernel's
+    need = lib.mla_chunk_workspace_size(ctypes.byref(bf), 4, 0)
+    assert need > 0 and chunk(lib, bf, window, ws_bytes=need - 1) == abi.MLA_ERR_WORKSPACE
+    assert need == lib.mla_chunk_workspace_size(ctypes.byref(bf), 1 << 20, 0)           # does not grow with the tokens
+    assert lib.mla_chunk_workspace_size(ctypes.byref(bf), 4, 3) < need
+    assert lib.mla_chunk_workspace_size(ctypes.byref(bf), -1, 0) == 0
+    for kw in (dict(n_tok=0), dict(batch=0)):                                           # nothing to do
+        assert chunk(lib, bf, window, **kw) == abi.MLA_OK
+
+
+def test_window_and_sinks_are_checked(lib):
+    for window in ((0, 0), (-1, 0), (5, -1)):
+        assert chunk(lib, _cfg(), window) == abi.MLA_ERR_INVALID_ARG
+
+
+def test_tables_refuse_bad_arguments(lib):
+    c = _cfg()
+    base = dict(batch=2, cached=OK, new=OK, free=OK, n_free=4, head=OK, num_blocks=8, table=OK, width=3, n_tok=5, cu=OK,
+                lens=OK, idx=OK, pos=OK, slots=OK, out=OK)
+
+    def call(**kw):
+        a = {**base, **kw}
+        return lib.mla_batch_tables(ctypes.byref(c), a["batch"], a["cached"], a["new"], a["free"], a["n_free"], a["head"],
+                                    a["num_blocks"], a["table"], a["width"], a["n_tok"], a["cu"], a["lens"], a["idx"],
+                                    a["pos"], a["slots"], a["out"], None)
+    for kw in (dict(batch=-1), dict(n_free=-1), dict(num_blocks=0), dict(width=0), dict(n_tok=-1), dict(cached=None),
+               dict(new=None), dict(free=None), dict(head=None), dict(table=None), dict(cu=None), dict(lens=None), dict(idx=None),
+               dict(pos=None), dict(slots=None), dict(out=None), dict(slots=OK + 4), dict(pos=OK + 2), dict(batch=0)):
+        assert call(**kw) == abi.MLA_ERR_INVALID_ARG, kw
+    assert call(batch=20000) == abi.MLA_ERR_UNSUPPORTED
+    assert call(width=1 << 26) == abi.MLA_ERR_UNSUPPORTED
+    assert call(batch=0, n_tok=0) == abi.MLA_OK
+
+
+def test_slots_and_stored_projection_refuse_bad_arguments(lib):
+    c, P = _cfg(), ctypes.byref
+    cache = abi.MLACache(OK, 8, OK, 2, 3)
+    need = lib.mla_cache_append_workspace_size(P(c), 4)
+    call = lambda pos=OK, slots=OK, ws=OK, n=need: lib.mla_cache_append_slots(P(c), OK, 4, OK, OK, pos, slots, P(cache), ws, n,
+                                                                              None)
+    for kw in (dict(pos=None), dict(slots=None), dict(ws=None), dict(slots=OK + 4), dict(pos=OK + 1)):
+        assert call(**kw) == abi.MLA_ERR_INVALID_ARG
+    assert call(n=need - 1) == abi.MLA_ERR_WORKSPACE
+    need = lib.mla_out_proj_workspace_size(P(c), 4)
+    assert lib.mla_out_proj_stored(P(c), ODD, 4, OK, OK, OK, OK, need, None) == abi.MLA_ERR_INVALID_ARG
+    assert lib.mla_out_proj_stored(P(c), OK, 4, OK, OK, OK, OK, need - 1, None) == abi.MLA_ERR_WORKSPACE
+    assert lib.mla_out_proj_stored(P(c), None, 4, OK, OK, OK, OK, need, None) == abi.MLA_ERR_INVALID_ARG
+    assert lib.mla_out_proj_stored(P(c), None, 0, None, None, None, None, 0, None) == abi.MLA_OK
