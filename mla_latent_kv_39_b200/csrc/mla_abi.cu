@@ -510,15 +510,24 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
                            (const float*)p.part_o, o_lat, lse));
 }
 
-template <typename TQ, typename T, typename TO>
+template <typename TQ, typename T, typename TO, int DPL>
 mla_status chunk_simt_launch(const chunk::SimtArgs& a, cudaStream_t s) {
-  const int row = a.d_c + a.d_r;
-  const size_t smem = sizeof(float) * ((size_t)row + (size_t)chunk::kSimtWarps * a.d_c);
-  const dim3 grid(a.q.n_tok, a.H), block(32 * chunk::kSimtWarps);
-  if (a.d_c <= 64) return st(launch_chained(chunk::chunk_simt_kernel<TQ, T, TO, 2>, grid, block, smem, s, a));
-  if (a.d_c <= 512) return st(launch_chained(chunk::chunk_simt_kernel<TQ, T, TO, 16>, grid, block, smem, s, a));
-  if (row <= kSimtDecodeMaxRow) return st(launch_chained(chunk::chunk_simt_kernel<TQ, T, TO, 32>, grid, block, smem, s, a));
-  return MLA_ERR_UNSUPPORTED;
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  const chunk::SimtShape g = chunk::simt_shape<T>(a.q.n_tok, a.H, a.d_c + a.d_r, sms);
+  const size_t smem = g.total(a.d_c);
+  static std::atomic<uint64_t> attr{0};
+  if (smem > 40 * 1024)  // with the static part, over the 48 KiB that need no asking
+    MLA_TRY(pairdec::set_smem_once((const void*)chunk::chunk_simt_kernel<TQ, T, TO, DPL>, 200 * 1024, attr));
+  return st(launch_chained(chunk::chunk_simt_kernel<TQ, T, TO, DPL>,
+                           dim3(a.q.n_tok, (a.H + g.heads - 1) / g.heads), dim3(32 * chunk::kSimtWarps),
+                           smem, s, a, g));
+}
+
+template <typename TQ, typename T, typename TO>
+mla_status chunk_simt_columns(const chunk::SimtArgs& a, cudaStream_t s) {
+  if (a.d_c <= 64) return chunk_simt_launch<TQ, T, TO, 2>(a, s);
+  if (a.d_c <= 512) return chunk_simt_launch<TQ, T, TO, 16>(a, s);
+  return chunk_simt_launch<TQ, T, TO, 32>(a, s);
 }
 
 mla_status chunk_simt_impl(const mla_config* c, const void* q, const void* q_rope, const chunk::Batch& b,
@@ -552,9 +561,9 @@ mla_status chunk_simt_impl(const mla_config* c, const void* q, const void* q_rop
   a.scale_log2 = scale_of(c) * 1.4426950408889634f;
   a.o_lat = o_lat;
   a.lse = lse;
-  if (fp8_cache(c)) return chunk_simt_launch<float, __nv_fp8_e4m3, bf16>(a, s);
-  if (c->dtype == MLA_BF16) return chunk_simt_launch<bf16, bf16, bf16>(a, s);
-  return chunk_simt_launch<float, float, float>(a, s);
+  if (fp8_cache(c)) return chunk_simt_columns<float, __nv_fp8_e4m3, bf16>(a, s);
+  if (c->dtype == MLA_BF16) return chunk_simt_columns<bf16, bf16, bf16>(a, s);
+  return chunk_simt_columns<float, float, float>(a, s);
 }
 
 mla_status chunk_impl(const mla_config* c, const void* q, const void* q_rope, int n_tok, const int32_t* cu_q, int batch,
