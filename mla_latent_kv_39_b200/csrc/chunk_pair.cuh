@@ -115,6 +115,8 @@ constexpr size_t smem_bytes() {
   return sizeof(Smem<kSplit>) + 1024;
 }
 static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "over the 227 KiB per-block limit");
+static_assert(kSoftmaxWarps * 3 * 4096 <= 4 * (kKvSlot + kSlab) && kSoftmaxWarps * 3 * 4096 <= 7 * kKvSlot,
+              "the last output's room fits the ring");
 static_assert(sizeof(long long) * (kMaxBatch + 1) <= 4 * (kKvSlot + kSlab) &&
                   sizeof(long long) * (kMaxBatch + 1) <= 7 * kKvSlot,
               "the prefix sums fit the ring");
@@ -649,7 +651,6 @@ struct Softmax {
     __syncwarp();
   }
   __device__ void put(uint8_t* own, const uint32_t (&v)[32], const CUtensorMap* map, int x, int y) {
-    own_free();
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       *reinterpret_cast<uint4*>(own + lane * 128 + ((c ^ (lane & 7)) << 4)) =
@@ -662,7 +663,9 @@ struct Softmax {
     }
     __syncwarp();
   }
-  __device__ void write_out(uint8_t* own, const Piece& d) {
+  // `room`: 12 KiB more of this warp's where nothing is loaded any more (the ring,
+  // behind the last piece), so that no pass waits for the one before; or null.
+  __device__ void write_out(uint8_t* own, uint8_t* room, const Piece& d) {
     const float inv = d.inv();
     const int col = 256 * ch + 128 * half, row0 = head - lane;  // the warp's first head
     if (d.whole) {
@@ -678,7 +681,8 @@ struct Softmax {
           for (int k = 0; k < 16; ++k)
             v[16 * e + k] = pack_bf16x2(__uint_as_float(a[2 * k]) * inv, __uint_as_float(a[2 * k + 1]) * inv);
         }
-        put(own, v, omap, col + 64 * c, d.tok * kH + row0);
+        if (c > 0 && room == nullptr) own_free();
+        put(c > 0 && room != nullptr ? room : own, v, omap, col + 64 * c, d.tok * kH + row0);
       }
     } else {
 #pragma unroll 1
@@ -688,7 +692,8 @@ struct Softmax {
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * inv);
-        put(own, v, partmap, col + 32 * c, d.slot * kH + row0);
+        if (c > 0 && room == nullptr) own_free();
+        put(c > 0 && room != nullptr ? room + (c - 1) * 4096 : own, v, partmap, col + 32 * c, d.slot * kH + row0);
       }
     }
     tc_fence_before();
@@ -797,7 +802,7 @@ struct Softmax {
         tmem_wait_st();
       }
       if (close) {
-        write_out(own, open);
+        write_out(own, nullptr, open);
         store_lse(open);
         own_free();
       }
@@ -827,7 +832,7 @@ struct Softmax {
       open.sum = row_sum(sm.xl[i & 1]);
       open.m = m_used;
       store_lse(open);
-      write_out(own, open);
+      write_out(own, sm.ring[0] + (4 * ch + 2 * half + ((l >> 5) & 1)) * 3 * 4096, open);
     }
     if (one) bulk_wait_all();
     __syncwarp();
@@ -911,30 +916,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- merge
 // Joins the pieces of the tokens that several workers share:
 //   o_lat = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).
-// Grid (workers, heads / 4).  A token of few pieces is joined by the blocks of
-// the worker that begins it, four heads to a block, one to each 64 threads.  Of a
-// token of many pieces (a long request) the blocks of its first eight workers
-// take half a head each, the pieces dealt to the eight warps: 256 blocks that
-// read 75 KB each of 74 pieces (28 us by 32 blocks of whole heads, 13 us by 128 of
-// one head).  A thread owns 8 latent columns; three loads are in flight, under no
-// condition.  An idle worker's place counts as a piece without visible rows (lse
-// -inf).  Sums run in a fixed order.
-constexpr int kMergeThreads = 256, kMergeHeads = 4, kMergeFew = 8;
+// Grid (workers, 8); most calls' workers share few tokens or none, and a block
+// without work costs its launch, so there are few.  A token of few pieces is
+// joined by the blocks of the worker that begins it, four heads at a time, one to
+// each 64 threads.  Of a token of many pieces (a long request) the blocks of up
+// to 32 of its workers take half a head at a time, the pieces dealt to the eight
+// warps: 256 blocks that read 75 KB each of 74 pieces (28 us by 32 blocks of
+// whole heads, 13 us by 128 of one head).  A thread owns 8 latent columns; three
+// loads are in flight, under no condition.  An idle worker's place counts as a
+// piece without visible rows (lse -inf).  Sums run in a fixed order.
+constexpr int kMergeThreads = 256, kMergeY = 8, kMergeFew = 8, kMergeMost = 32;
 
-__global__ void __launch_bounds__(kMergeThreads, 6) chunk_merge_kernel(const int4* __restrict__ shares,
+__global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const int4* __restrict__ shares,
                                                                        const float* __restrict__ part_lse,
                                                                        const float* __restrict__ part_o,
                                                                        bf16* __restrict__ o_lat,
                                                                        float* __restrict__ lse_out) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float wt[kMaxWorkers + kMergeHeads * kMergeFew];  // weights: one list of many, or four of few
+  __shared__ float wt[kMaxWorkers + 4 * kMergeFew];  // weights: one list of many, or four of few
   __shared__ float4 sum[kMergeThreads / 32][2][32];
   const int w = blockIdx.x;
   int4 own = shares[w];
   int w0 = w;
   if (own.y < 0 || own.z - w0 < kMergeFew) {  // not the first worker of a token of many pieces: one of its next?
-    if (own.w >= 0 && w - own.w < kMergeFew) {
+    if (own.w >= 0 && w - own.w < kMergeMost) {
       const int4 head = shares[own.w];
       if (head.z - own.w >= kMergeFew) {
         w0 = own.w;
@@ -946,75 +952,83 @@ __global__ void __launch_bounds__(kMergeThreads, 6) chunk_merge_kernel(const int
   if (tok < 0) return;
   const bool many = n > kMergeFew;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int h = kMergeHeads * blockIdx.y + (many ? (w - w0) / 2 : warp / 2);
-  const int d = many ? kDc / 2 * ((w - w0) & 1) + 8 * lane : 8 * (threadIdx.x % 64);
+  // items: half a head of many pieces, four heads of few
+  const int helpers = many ? min(n, kMergeMost) : 1;
+  const int items = many ? 2 * kH : kH / 4, step_item = kMergeY * helpers;
   float* list = many ? wt : wt + kMergeFew * (warp / 2);
   // piece i: the beginning with worker w0, the rest with the workers behind it
   const auto slot_of = [&](int i) { return 2 * (w0 + i) + (i == 0 ? 1 : 0); };
-  if (many ? warp == 0 : warp % 2 == 0) {
-    float M = -INFINITY, Z = 0.f;
-    for (int i = lane; i < n; i += 32) {
-      const float x = part_lse[(long long)slot_of(i) * kH + h];
-      list[i] = x;
-      M = fmaxf(M, x);
-      if (x != x) Z = x;  // the maximum passes over NaN, the sum must not
-    }
-    M = warp_max(M);
-    for (int i = lane; i < n; i += 32) {
-      const float x = M == -INFINITY ? 0.f : exp2f(list[i] - M);  // M = -inf: no piece has a visible row
-      list[i] = x;
-      Z += x;
-    }
-    Z = warp_sum(Z);
-    const float inv = Z == 0.f ? 0.f : 1.f / Z;
-    for (int i = lane; i < n; i += 32) list[i] *= inv;
-    if (lse_out != nullptr && lane == 0 && d < kDc / 2)
-      lse_out[(long long)tok * kH + h] = Z == 0.f ? -INFINITY : M + log2f(Z);
-  }
-  __syncthreads();
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const auto add = [&](int i, const float4& x, const float4& y) {
-    const float f = i < n ? list[i] : 0.f;
-    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] = fmaf(f, f == 0.f ? 0.f : v[c], acc[c]);  // weight 0: nothing was written there
-  };
-  const auto at = [&](int i) {
-    return reinterpret_cast<const float4*>(part_o + ((long long)slot_of(min(i, n - 1)) * kH + h) * kDc + d);
-  };
-  const int step = many ? kMergeThreads / 32 : 1;
-  for (int i = many ? warp : 0; i < n; i += 3 * step) {
-    const float4 x0 = __ldcs(at(i)), y0 = __ldcs(at(i) + 1);
-    const float4 x1 = __ldcs(at(i + step)), y1 = __ldcs(at(i + step) + 1);
-    if (n > 2) {
-      const float4 x2 = __ldcs(at(i + 2 * step)), y2 = __ldcs(at(i + 2 * step) + 1);
-      add(i, x0, y0);
-      add(i + step, x1, y1);
-      add(i + 2 * step, x2, y2);
-    } else {
-      add(i, x0, y0);
-      add(i + 1, x1, y1);
-    }
-  }
-  if (many) {
-    sum[warp][0][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    sum[warp][1][lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    __syncthreads();
-    if (warp > 0) return;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int g = 1; g < kMergeThreads / 32; ++g) {
-        const float4 v = sum[g][e][lane];
-        acc[4 * e] += v.x;
-        acc[4 * e + 1] += v.y;
-        acc[4 * e + 2] += v.z;
-        acc[4 * e + 3] += v.w;
+  for (int it = blockIdx.y + kMergeY * (w - w0); it < items; it += step_item) {
+    const int h = many ? it / 2 : 4 * it + warp / 2;
+    const int d = many ? kDc / 2 * (it & 1) + 8 * lane : 8 * (threadIdx.x % 64);
+    if (many ? warp == 0 : warp % 2 == 0) {
+      float M = -INFINITY, Z = 0.f;
+      for (int i = lane; i < n; i += 32) {
+        const float x = part_lse[(long long)slot_of(i) * kH + h];
+        list[i] = x;
+        M = fmaxf(M, x);
+        if (x != x) Z = x;  // the maximum passes over NaN, the sum must not
       }
+      M = warp_max(M);
+      for (int i = lane; i < n; i += 32) {
+        const float x = M == -INFINITY ? 0.f : exp2f(list[i] - M);  // M = -inf: no piece has a visible row
+        list[i] = x;
+        Z += x;
+      }
+      Z = warp_sum(Z);
+      const float inv = Z == 0.f ? 0.f : 1.f / Z;
+      for (int i = lane; i < n; i += 32) list[i] *= inv;
+      if (lse_out != nullptr && lane == 0 && d < kDc / 2)
+        lse_out[(long long)tok * kH + h] = Z == 0.f ? -INFINITY : M + log2f(Z);
+    }
+    __syncthreads();
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const auto add = [&](int i, const float4& x, const float4& y) {
+      const float f = i < n ? list[i] : 0.f;
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] = fmaf(f, f == 0.f ? 0.f : v[c], acc[c]);  // weight 0: nothing was written there
+    };
+    const auto at = [&](int i) {
+      return reinterpret_cast<const float4*>(part_o + ((long long)slot_of(min(i, n - 1)) * kH + h) * kDc + d);
+    };
+    const int step = many ? kMergeThreads / 32 : 1;
+    for (int i = many ? warp : 0; i < n; i += 3 * step) {
+      const float4 x0 = __ldcs(at(i)), y0 = __ldcs(at(i) + 1);
+      const float4 x1 = __ldcs(at(i + step)), y1 = __ldcs(at(i + step) + 1);
+      if (n > 2) {
+        const float4 x2 = __ldcs(at(i + 2 * step)), y2 = __ldcs(at(i + 2 * step) + 1);
+        add(i, x0, y0);
+        add(i + step, x1, y1);
+        add(i + 2 * step, x2, y2);
+      } else {
+        add(i, x0, y0);
+        add(i + 1, x1, y1);
+      }
+    }
+    if (many) {
+      sum[warp][0][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      sum[warp][1][lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int g = 1; g < kMergeThreads / 32; ++g) {
+            const float4 v = sum[g][e][lane];
+            acc[4 * e] += v.x;
+            acc[4 * e + 1] += v.y;
+            acc[4 * e + 2] += v.z;
+            acc[4 * e + 3] += v.w;
+          }
+      }
+    }
+    if (!many || warp == 0)
+      *reinterpret_cast<uint4*>(o_lat + ((long long)tok * kH + h) * kDc + d) =
+          make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                     pack_bf16x2(acc[6], acc[7]));
+    __syncthreads();  // the lists are read before the next item's are made
   }
-  *reinterpret_cast<uint4*>(o_lat + ((long long)tok * kH + h) * kDc + d) =
-      make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
-                 pack_bf16x2(acc[6], acc[7]));
 }
 
 // ================================================================ host side

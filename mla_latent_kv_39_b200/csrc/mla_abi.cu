@@ -505,7 +505,7 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
     MLA_TRY((split ? chunk_pair_launch<true, chunk::PoolMap>(k, m, p, s)
                    : chunk_pair_launch<false, chunk::PoolMap>(k, m, p, s)));
   if (whole) return MLA_OK;
-  return st(launch_chained(chunk::chunk_merge_kernel, dim3(workers, chunk::kH / chunk::kMergeHeads),
+  return st(launch_chained(chunk::chunk_merge_kernel, dim3(workers, chunk::kMergeY),
                            dim3(chunk::kMergeThreads), 0, s, (const int4*)p.shares, (const float*)p.part_lse,
                            (const float*)p.part_o, o_lat, lse));
 }
