@@ -209,9 +209,9 @@ __host__ __device__ inline Found place_at(const Batch& q, const Cut& cut, const 
   }
   int k = 0;
   if (f.s.p0 >= 0 && !cut.single) {
-    const long long i = (r - cut.tokens(q.vis, f.s, a) - kTokenCost) / kFullTile;  // rounds towards 0
+    const long long i = r - cut.tokens(q.vis, f.s, a) - kTokenCost;  // below 0 in the token's fixed cost
     const int n = q.vis.tiles(f.s.p0 + a);
-    k = (i < n ? (int)i : n - 1) * kTilePages;
+    k = i < 0 ? 0 : (int)(i / kFullTile < n ? i / kFullTile : n - 1) * kTilePages;
   }
   f.at = {lo, a, k};
   return f;
