@@ -69,7 +69,7 @@ constexpr int kSlabs = kRow / 64;
 constexpr int kSlab = 64 * 128;  // 64 rows x 64 bf16, 128-byte swizzle
 constexpr int kKvSlot = 2 * kSlab;
 constexpr int kTmemS = 0, kTmemO = 256, kTmemCols = 512;
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp0 = 9, kLoadWarps = 2, kQueryWarp = 11;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp0 = 9, kLoadWarps = 2, kPlanWarp = 11;
 constexpr int kThreads = 32 * 12;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint16_t kBoth = 3;
@@ -85,7 +85,7 @@ struct Geo {
 };
 
 // A tile as the load, MMA and softmax warps of a CTA need it, planned by its
-// query warp up to kTiles ahead; one with n = 0 comes behind the last.
+// plan warp up to kTiles ahead; one with n = 0 comes behind the last.
 struct Tile {
   int n;                   // items
   int first, last, whole;  // the tile begins / ends its piece; the piece is the whole token
@@ -879,7 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(&sm.tmem_base, kTmemCols);
     tmem_relinquish_pair();
   }
-  if (warp == kQueryWarp && lane == 0) {
+  if (warp == kPlanWarp && lane == 0) {
     prefetch_tensormap(&pool.end[sizeof(Maps) / sizeof(CUtensorMap) - 1]);
     prefetch_tensormap(&qmap);
   }
@@ -898,7 +898,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!so.run()) set_abort(sm);
   } else if (warp == kMmaWarp) {
     if (rank == 0) mma_role(sm, tmem, p);
-  } else if (warp == kQueryWarp) {
+  } else if (warp == kPlanWarp) {
     plan_role<kSplit, Maps>(sm, &qmap, p, rank, worker, lane);
   } else {
     load_role<kSplit, Maps>(sm, pool, &qlomap, p, warp - kLoadWarp0, rank, lane);

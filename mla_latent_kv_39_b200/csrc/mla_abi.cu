@@ -494,7 +494,8 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
                         reinterpret_cast<float*>(base + L.off_o), o_lat, lse};
   CUtensorMap m[4];  // queries, their low parts, output, pieces
   MLA_TRY(pairdec::query_map(q, b.n_tok, &m[0]));
-  MLA_TRY(pairdec::query_map(split ? q + (long long)b.n_tok * chunk::kH * chunk::kRow : q, b.n_tok, &m[1]));
+  m[1] = m[0];
+  if (split) MLA_TRY(pairdec::query_map(q + (long long)b.n_tok * chunk::kH * chunk::kRow, b.n_tok, &m[1]));
   MLA_TRY(chunk::out_map(o_lat, (long long)b.n_tok * chunk::kH, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, &m[2]));
   MLA_TRY(chunk::out_map(p.part_o, 2LL * workers * chunk::kH, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, &m[3]));
   // only a window shorter than a page cuts a page's rows on both sides
