@@ -431,9 +431,9 @@ mla_status mla_combine_out_proj(const mla_config* cfg, const void* decode_ws, si
  *
  * mla_cache_append_slots - mla_cache_append with the tokens' slots given
  * instead of (sequence, position): row t goes to slot slots[t]; a slot of -1
- * stores nothing (padding).  pos is the rotation's position.  Any other slot
- * outside the pool -> MLA_ERR_BOUNDS, row not written.  Workspace as
- * mla_cache_append.
+ * stores nothing (padding).  pos is the rotation's position.  The stored slots
+ * of a call must differ.  Any other slot outside the pool -> MLA_ERR_BOUNDS, row
+ * not written.  Workspace as mla_cache_append.
  * ------------------------------------------------------------------------- */
 mla_status mla_batch_tables(const mla_config* cfg, int32_t batch, const int32_t* cached_lens,
                             const int32_t* new_lens, const int32_t* free_blocks, int32_t n_free,
@@ -473,7 +473,8 @@ mla_status mla_cache_append_slots(const mla_config* cfg, const void* x, int32_t 
  *            Rows from cu_q[batch] on are left as they are.
  *   max_workers: upper bound on parallel workers (0 = the device's).
  *   workspace >= mla_chunk_workspace_size(cfg, n_tok, max_workers); it does
- *            not grow with the lengths.
+ *            not grow with the lengths and need not be initialised.  Calls that
+ *            may overlap on the GPU need one each.
  * 128 heads, d_c 512, d_r 64, pages of 64 and a bf16 cache run on the tensor
  * cores; every other shape on CUDA cores (d_c + d_r <= 1024, any block_size).
  * For a large FP8 cache expand the pages first (mla_cache_dequant_fp8).

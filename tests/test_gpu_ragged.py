@@ -398,3 +398,84 @@ def test_batch_tables_reports_bad_entries():
     got = t.run()
     assert mla_get_device_error()[0] == abi.MLA_ERR_BOUNDS
     assert (got["slots"][:10] == -1).all() and (got["slots"][10:] >= 0).all()
+
+
+def test_tables_at_the_largest_batch():
+    n = 16384
+    cached = [(7 * b) % 130 for b in range(n)]
+    new = [(b * b) % 3 for b in range(n)]
+    t = Tables(cached, new, pad=5)
+    t.check()
+    t.check(in_place=True)
+    check_device_error()
+
+
+@pytest.mark.parametrize("batch", [33, 1000, 8192])
+def test_large_batches_with_few_tokens(batch):
+    new = [1 if b % (batch // 20) == 7 else 0 for b in range(batch)]
+    new[-1] = 40
+    cached = [(3 * b) % 200 if new[b] else 5 for b in range(batch)]
+    r = Ragged(Config(**V3), cached, new, 2)
+    r.run()
+    check_device_error()
+    r.check()
+    r.run(50, 3)
+    check_device_error()
+    r.check(50, 3)
+
+
+@pytest.mark.parametrize("heads", [128, 2])
+def test_caches_past_32_bits(heads):
+    """Pages more than 4 GiB into the pool (and more than 2^31 values)."""
+    r = Ragged(Config(**{**V3, "n_heads": heads}), [300, 64], [3, 1], 1)
+    far = 65000
+    pool = torch.zeros(far + r.pool.shape[0], 64, 576, dtype=torch.bfloat16, device="cuda")
+    assert pool.numel() * 2 > 2 ** 32
+    pool[far:] = r.pool
+    r.table = torch.where(r.table >= 0, r.table + far, r.table)
+    r.cache = Cache(pool, r.table)
+    for window, sinks in ((0, 0), (100, 5)):
+        r.run(window, sinks)
+        check_device_error()
+        r.check(window, sinks)
+
+
+def test_one_workspace_under_two_graphs():
+    a = Ragged(Config(**V3), [6000, 10], [1, 30], 4, seed=1)
+    b = Ragged(Config(**V3), [100, 9000], [50, 1], 0, seed=2)
+    b.ws = a.ws
+    a.run()
+    b.run(3000, 4)
+    torch.cuda.synchronize()
+    graphs = []
+    for f in (lambda: a.run(), lambda: b.run(3000, 4)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            f()
+        graphs.append(g)
+    for order in ((0, 1), (1, 0, 0, 1)):
+        for x in (a, b):
+            x.o_lat.fill_(7)
+            x.lse.fill_(7)
+        for k in order:
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        check_device_error()
+        a.check()
+        b.check(3000, 4)
+
+
+def test_inputs_of_another_stream():
+    """The call takes its stream as an argument: work queued there before it is waited for, the current stream's is not needed."""
+    r = Ragged(Config(**V3), [700, 64], [5, 1], 1)
+    good = r.q.clone()
+    r.q.fill_(float("nan"))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        r.q.copy_(good)
+    r.run(stream=s)
+    s.synchronize()
+    check_device_error()
+    r.check()
