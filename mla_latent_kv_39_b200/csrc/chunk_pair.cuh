@@ -95,6 +95,10 @@ struct Tile {
 };
 constexpr int kTiles = 4;
 
+// What the costs come to, over a warp's sequences.
+struct Sums {
+  long long cost, tokens, longest;
+};
 template <bool kSplit>
 struct Smem {
   using G = Geo<kSplit>;
@@ -104,6 +108,7 @@ struct Smem {
   uint64_t full[G::kSlots], empty[G::kSlots];
   uint64_t q_full, q_empty, s_full[2], p_full, pv_done, fin, xbar[2], lbar, tile_full[kTiles], tile_empty[kTiles];
   Tile tile[kTiles];
+  Sums sums[kThreads / 32];
   float xm[2][2][128];                       // [tile parity][column half] maximum of each lane's columns
   float xl[2][2][128];                       // [tile parity][column half] shares of a finished piece's row sums
   uint32_t tmem_base;
@@ -221,15 +226,16 @@ __device__ __forceinline__ Found found_of(const Found& f, int lane) {
   return r;
 }
 
-// The two ends of this worker's range, by one warp: costs of the sequences, a
-// run of them to a lane, summed up in `C` (shared memory); then lane 0 looks for
-// the one end and lane 1 for the other.
-__device__ __forceinline__ Cut find_range(const Params& p, long long* C, int worker, int lane, Found& from, Found& to) {
+// The costs of the sequences, summed up in `C` (shared memory), a run of them to
+// each of kIds threads: a warp or, with `sums`, the whole block.
+template <int kIds>
+__device__ __forceinline__ Cut sum_costs(const Params& p, long long* C, Sums* sums) {
   const Batch& q = p.q;
-  const int per = (q.batch + 31) / 32, b0 = min(lane * per, q.batch), b1 = min(b0 + per, q.batch);
+  const int id = threadIdx.x % kIds, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (q.batch + kIds - 1) / kIds, b0 = min(id * per, q.batch), b1 = min(b0 + per, q.batch);
   Cut cut{0, p.workers, p.inv_workers, 0};
   long long mine = 0, longest = 0;
-  long long own = 0;  // tokens of this lane's run
+  long long own = 0;  // tokens of this thread's run
   for (int b = b0; b < b1; ++b) {
     const Sequence s = sequence_of(q, b);
     if (blockIdx.x == 0) report_sequence(q, b, s);
@@ -251,8 +257,23 @@ __device__ __forceinline__ Cut find_range(const Params& p, long long* C, int wor
     longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
   }
   cut.total = shfl64(x, 31);
+  long long tokens = shfl64(t, 31);
+  if constexpr (kIds > 32) {
+    if (lane == 0) sums[warp] = Sums{cut.total, tokens, longest};
+    __syncthreads();
+    cut.total = tokens = 0;
+    for (int w = 0; w < kIds / 32; ++w) {
+      const Sums o = sums[w];
+      if (w < warp) {
+        x += o.cost;
+        t += o.tokens;
+      }
+      cut.total += o.cost;
+      tokens += o.tokens;
+      longest = max(longest, o.longest);
+    }
+  }
   long long ahead = x - mine;
-  const long long tokens = shfl64(t, 31);
   if (p.single || one_token_each(tokens, cut.total, longest, p.workers)) {
     cut.single = 1;
     cut.total = tokens;
@@ -261,13 +282,32 @@ __device__ __forceinline__ Cut find_range(const Params& p, long long* C, int wor
     for (int b = b0; b < b1; ++b) C[b + 1] = mine += sequence_of(q, b).n;
   }
   for (int b = b0; b < b1; ++b) C[b + 1] += ahead;
-  if (lane == 0) C[0] = 0;
-  __syncwarp();
-  const Found f = place_at(q, cut, C, cut.at(worker + (lane & 1)));
+  if (id == 0) C[0] = 0;
+  return cut;
+}
+
+// Up to kWarpBatch sequences the plan warp does it alone while the others go to
+// their roles; above, the whole block does it ahead of the roles.  A call with 16
+// new tokens takes, by warp and by block, 21.8 and 23.4 us for 64 sequences, 22.5
+// and 23.5 for 128, 24.2 and 23.7 for 256, 28.6 and 24.4 for 512; for 8192 of
+// 100 rows 230 and 48.  Out of line, so that it does not weigh on the registers of
+// what follows (inlined: 4 us more on a decode step of 100,000 rows).
+constexpr int kWarpBatch = 128;
+static __device__ __noinline__ Cut sum_costs_of_block(const Params& p, long long* C, Sums* sums) {
+  const Cut cut = sum_costs<kThreads>(p, C, sums);
+  fence_proxy_async_smem();  // the sums give way to the ring's loads
+  __syncthreads();
+  return cut;
+}
+
+// The two ends of this worker's range, by one warp: lane 0 looks for the one end
+// and lane 1 for the other.
+__device__ __forceinline__ void find_range(const Params& p, const Cut& cut, const long long* C, int worker, int lane,
+                                           Found& from, Found& to) {
+  const Found f = place_at(p.q, cut, C, cut.at(worker + (lane & 1)));
   from = found_of(f, 0);
   to = found_of(f, 1);
   __syncwarp();
-  return cut;
 }
 
 // ---------------------------------------------------------------- tile records
@@ -384,7 +424,8 @@ __device__ void load_role(Smem<kSplit>& sm, const Maps& pool, const CUtensorMap*
 // them, writes the rows of tokens that see nothing (zeros, log-sum-exp of an
 // empty set) and what the merge needs to know.
 template <bool kSplit, typename Maps>
-__device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, int rank, int worker, int lane) {
+__device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Params& p, Cut cut, int rank, int worker,
+                          int lane) {
   constexpr int kWhole = sizeof(Maps) / sizeof(CUtensorMap) - 1;
   const bool one = elect_one();
   int pieces = 0, i = 0;
@@ -403,8 +444,13 @@ __device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Param
     }
     __syncwarp();
   };
+  long long* C = reinterpret_cast<long long*>(sm.ring);
+  if (p.q.batch <= kWarpBatch) {
+    cut = sum_costs<32>(p, C, nullptr);
+    __syncwarp();
+  }
   Found from, to;
-  const Cut cut = find_range(p, reinterpret_cast<long long*>(sm.ring), worker, lane, from, to);
+  find_range(p, cut, C, worker, lane, from, to);
   fence_proxy_async_smem();  // the prefix sums give way to the ring's loads
   __syncwarp();
   for (Walk w(p.q, from.at, from.s, to.at); w.valid(); w.next()) {
@@ -890,6 +936,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uni(sm.tmem_base);
   pdl_wait();  // the queries, the tables and the appended rows come from the kernels before
   pdl_trigger();
+  Cut cut{};
+  if (p.q.batch > kWarpBatch) cut = sum_costs_of_block(p, reinterpret_cast<long long*>(sm.ring), sm.sums);
 
   if (warp < kSoftmaxWarps) {
     const int l = (warp & 3) * 32 + lane;
@@ -899,7 +947,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     if (rank == 0) mma_role(sm, tmem, p);
   } else if (warp == kPlanWarp) {
-    plan_role<kSplit, Maps>(sm, &qmap, p, rank, worker, lane);
+    plan_role<kSplit, Maps>(sm, &qmap, p, cut, rank, worker, lane);
   } else {
     load_role<kSplit, Maps>(sm, pool, &qlomap, p, warp - kLoadWarp0, rank, lane);
   }

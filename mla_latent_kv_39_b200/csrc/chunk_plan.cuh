@@ -245,12 +245,30 @@ struct Walk {
     s.n = uni(s.n);
     s.p0 = uni(s.p0);
   }
+  // the first sequence from b on that seems to have tokens (batch: none), 32 at a look
+  __host__ __device__ int filled(int b) const {
+#ifdef __CUDA_ARCH__
+    for (; b < q.batch; b += 32) {
+      const int i = b + (threadIdx.x & 31);
+      const uint32_t some = __ballot_sync(0xffffffffu, i < q.batch && q.cu_q[i] < q.cu_q[i + 1]);
+      if (some != 0) return b + __ffs(some) - 1;
+    }
+    return q.batch;
+#else
+    while (b < q.batch && q.cu_q[b] >= q.cu_q[b + 1]) ++b;
+    return b;
+#endif
+  }
   // bring `at` to a token that exists, and measure its piece
   __host__ __device__ void settle() {
     while (valid() && at.j >= s.n) {
       at.j = 0;
       at.k = 0;
       if (++at.b >= q.batch) return;  // `to` is at most (batch, 0, 0): not valid any more
+      load();
+      if (s.n > 0) continue;
+      at.b = filled(at.b + 1);
+      if (at.b >= q.batch) return;
       load();
     }
     if (!valid()) return;
