@@ -420,7 +420,8 @@ mla_status mla_combine_out_proj(const mla_config* cfg, const void* decode_ws, si
  *   free_head_out  int32 [1]     *free_head plus the pages taken (may be free_head itself)
  *   num_blocks: blocks of the pool, to check block ids against.
  * Any other overlap of outputs with inputs or with one another is not allowed.
- * batch <= 16384, max_blocks_per_seq * block_size < 2^31 (MLA_ERR_UNSUPPORTED).
+ * batch <= 16384, max_blocks_per_seq * block_size < 2^31 - block_size
+ * (MLA_ERR_UNSUPPORTED); batch 0 only with n_tok 0, a call without effect.
  * Device errors (MLA_ERR_BOUNDS):
  *   - a negative length, or more rows than a table row holds: that request
  *     gets no tokens and seq_lens 0;

@@ -448,6 +448,7 @@ def mla_out_proj(cfg: Config, o_lat, W_UV, W_O, y, workspace, stream=None):
 
 
 # --------------------------------------------------------------- ragged steps
+MAX_CHUNK_BATCH = 8192        # sequences of a ragged attention call
 
 def _need_here(*tensors):
     """Every given tensor is on the current device (the library launches there)."""

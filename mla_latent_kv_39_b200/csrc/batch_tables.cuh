@@ -16,9 +16,11 @@
 // the requests.
 //
 // What bounds it is latency: 8 bytes read a request, 16 bytes written a token.
-// One cluster of up to 8 CTAs, each of which makes both prefix sums for itself
+// One cluster of 8 CTAs, each of which makes both prefix sums for itself
 // (a scan of at most 16,384 values costs less than handing them round) and
-// then fills its share of the tokens.  Inputs that an output may replace (the
+// then fills its share of the tokens: 3.5 us in a graph for 64 requests of a token
+// each (one CTA alone 3.6), 4.5 for 512 of 16 (13.2), 11.3 for 64 of 1024 (66),
+// 18.4 for 16,384 of one (72).  Inputs that an output may replace (the
 // lengths by seq_lens, the cursor by its new value) are read by all CTAs before
 // the cluster's barrier and written behind it; one launch and no workspace.
 #pragma once
@@ -30,6 +32,7 @@ namespace tables {
 
 constexpr int kMaxBatch = 16384;  // requests of a call: two prefix sums in shared memory
 constexpr int kThreads = 1024;
+constexpr int kCtas = 8;
 
 struct Args {
   int batch, bs, n_free, num_blocks, max_blocks, n_tok;
@@ -100,17 +103,21 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
   const bool bad_head = head < 0 || head > a.n_free;
   if (bad_head) head = a.n_free;  // nothing to hand out
   const int avail = a.n_free - head;
-  const int per = pages_of(a.batch, kThreads);
+  // every request's own counts, until the scan
+#pragma unroll 4
+  for (int b = tid; b < a.batch; b += kThreads) {
+    const int c = a.cached[b], w = a.new_[b];
+    const bool bad = c < 0 || w < 0 || (long long)c + w > (long long)a.max_blocks * a.bs;
+    len[b] = bad ? -1 : c;
+    cu[b + 1] = bad ? 0 : w;
+    first[b + 1] = bad ? 0 : pages_of(c + w, a.bs) - pages_of(c, a.bs);
+  }
+  const int per = pages_of(a.batch, kThreads) | 1;  // odd: the threads' runs begin in different banks
+  if (per > 1) __syncthreads();
   const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
   long long n = 0, pages = 0;
   for (int b = b0; b < b1; ++b) {
-    const int c = a.cached[b], w = a.new_[b];
-    const bool bad = c < 0 || w < 0 || (long long)c + w > (long long)a.max_blocks * a.bs;
-    if (bad && rank == 0) report(MLA_ERR_BOUNDS, 30, b, c < 0 ? c : w);
-    len[b] = bad ? -1 : c;
-    // until the scan: this request's own counts
-    cu[b + 1] = bad ? 0 : w;
-    first[b + 1] = bad ? 0 : pages_of(c + w, a.bs) - pages_of(c, a.bs);
+    if (len[b] < 0 && rank == 0) report(MLA_ERR_BOUNDS, 30, b, a.cached[b] < 0 ? a.cached[b] : a.new_[b]);
     n += cu[b + 1];
     pages += first[b + 1];
   }
@@ -192,10 +199,6 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
   }
 }
 
-// CTAs of the cluster: one fills 4,096 tokens in four rounds of its threads;
-// beyond that more of them share the tokens.
-inline int ctas_for(int n_tok) { return n_tok <= 4 * kThreads ? 1 : 8; }
-
 inline mla_status launch(const Args& a, cudaStream_t s) {
   const size_t smem = sizeof(int) * (3 * (size_t)a.batch + 2);
   static std::atomic<uint64_t> attr{0};
@@ -203,7 +206,7 @@ inline mla_status launch(const Args& a, cudaStream_t s) {
       pairdec::set_smem_once((const void*)batch_tables_kernel, sizeof(int) * (3 * (size_t)kMaxBatch + 2), attr) != MLA_OK)
     return MLA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas_for(a.n_tok));
+  cfg.gridDim = dim3(kCtas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

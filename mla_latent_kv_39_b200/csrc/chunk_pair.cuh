@@ -21,15 +21,29 @@
 //
 // Every operand slab is loaded by TMA into one ring of 16 KiB slots in the
 // order in which the MMAs take them:
-//   K(0), K(1), V(0), K(2), V(1), ...   (9 slots for K, 2 per page for V),
+//   K(0), K(1), V(0), K(2), V(1), ...   (9 slots for K, 2 per page for V;
+//   7 slots: 8 or 9 gained under 1%, 6 and 5 cost 2 and 9%),
 // and the MMAs are issued in that order by one warp: the scores of tile i + 1
 // run ahead of P V of tile i, into the other of two score buffers, so the
 // softmax of a tile has the time of two MMA phases.  Keys are read a second
 // time as values (an L2 hit): holding them from the scores to P V would take
-// two tiles of shared memory, and the ring streams faster than the MMAs need.
-// One warp issues a load and its barrier work in about 420 clocks (19 B per
-// clock and SM), four warps 77 B per clock, so four warps take the ring's
-// slots in turn.
+// two tiles of shared memory.  Two warps take the ring's slots in turn, the
+// loads issued under elect.sync (under `lane == 0` a load and its barrier work
+// took 420 clocks, 19 B per clock and SM).
+//
+// What bounds it is the bandwidth of shared memory.  A tile moves 724 KB through
+// each SM's: 414 KB of operands into the MMAs, 278 KB from TMA, 32 KB of P.  At
+// 128 B per clock that is 5,656 clocks; measured are 5,620 a tile, with the
+// tensor pipe at 68% over a whole call (its own time is 4,352).  8 sequences of
+// 64 new tokens over 1k to 4k rows (315 GFLOP) take 266 us, 1.18 PFLOP/s; 1,024
+// new tokens of a 16k request (4.53 TFLOP) 3.35 ms, 1.35 PFLOP/s, by then at the
+// clock that the power limit leaves.  Decode steps are bound by the reads of
+// their pages from memory behind some 15 us of launch, planning and output.
+//
+// Measured and left out: pages fetched into L2 ahead (56 -> 65 us on a decode
+// step of 64 requests); scores two tiles ahead, the output kept in registers or
+// set aside in TMEM across pieces (1 to 14% slower); four load warps, eight more
+// warps for the output (2 to 6% slower).
 //
 // TMEM (512 columns): scores [0, 128) and [128, 256), output [256, 512).
 // A pair MMA of M = 128 leaves a CTA's 64 rows in 128 lanes x N / 2 columns:

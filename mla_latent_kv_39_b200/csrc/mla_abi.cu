@@ -489,9 +489,20 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
   const bool whole = b.n_tok <= workers && b.vis.most_cost(b.max_rows) <= chunk::kSplitCost;
   if (whole) workers = b.n_tok;
   char* base = static_cast<char*>(ws);
-  const chunk::Params p{b, k->block_table, k->max_blocks_per_seq, k->num_blocks, scale_of(c) * 1.4426950408889634f, g_wait_limit_ns.load(std::memory_order_relaxed), workers,
-                        1.f / workers, whole ? 1 : 0, reinterpret_cast<int4*>(base + L.off_shares), reinterpret_cast<float*>(base + L.off_lse),
-                        reinterpret_cast<float*>(base + L.off_o), o_lat, lse};
+  const chunk::Params p{b,
+                        k->block_table,
+                        k->max_blocks_per_seq,
+                        k->num_blocks,
+                        scale_of(c) * 1.4426950408889634f,
+                        g_wait_limit_ns.load(std::memory_order_relaxed),
+                        workers,
+                        1.f / workers,
+                        whole ? 1 : 0,
+                        reinterpret_cast<int4*>(base + L.off_shares),
+                        reinterpret_cast<float*>(base + L.off_lse),
+                        reinterpret_cast<float*>(base + L.off_o),
+                        o_lat,
+                        lse};
   CUtensorMap m[4];  // queries, their low parts, output, pieces
   MLA_TRY(pairdec::query_map(q, b.n_tok, &m[0]));
   m[1] = m[0];

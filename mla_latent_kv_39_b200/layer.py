@@ -272,12 +272,18 @@ class RaggedLayer:
     from ``free_blocks``), projects the queries, stores the new latent rows
     through their slots, attends (causally, or over a sliding window and a few
     first rows) and projects the output.  ``cache.block_table`` is extended in
-    place.  ``window`` = 0: all rows up to the token's own."""
+    place.  ``window`` = 0: all rows up to the token's own.
+
+    Pages that have left a window may be given to other requests, with any entry
+    left in the table; not so with an FP8 cache, whose step expands all pages
+    that the lengths cover."""
 
     def __init__(self, cfg: abi.Config, weights: Dict[str, torch.Tensor], cache: abi.Cache, n_tok: int,
                  window: int = 0, n_sinks: int = 0, max_workers: int = 0):
-        if window < 0 or n_sinks < 0:
-            raise ValueError("window and n_sinks must not be negative")
+        if window < 0 or n_sinks < 0 or max_workers < 0:
+            raise ValueError("window, n_sinks and max_workers must not be negative")
+        if cache.block_table.shape[0] > abi.MAX_CHUNK_BATCH:
+            raise ValueError(f"at most {abi.MAX_CHUNK_BATCH} requests a step, got {cache.block_table.shape[0]}")
         self.cfg, self.W, self.cache, self.n_tok = cfg, weights, cache, n_tok
         self.window, self.n_sinks, self.max_workers = window, n_sinks, max_workers
         dev, H = cache.pool.device, cfg.n_heads

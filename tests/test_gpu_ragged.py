@@ -424,6 +424,21 @@ def test_large_batches_with_few_tokens(batch):
     r.check(50, 3)
 
 
+@pytest.mark.parametrize("batch", [128, 129, 400])
+def test_large_batches_whose_tokens_are_cut(batch):
+    """More sequences than the plan warp sums up alone, a few of them long enough to be shared by workers."""
+    new = [0 if b % 5 == 0 else 1 + (b * b) % 3 for b in range(batch)]
+    cached = [(37 * b) % 150 for b in range(batch)]
+    for b in (3, batch - 2):
+        new[b], cached[b] = 2, 9000
+    cached[6], new[6] = 0, 70
+    r = Ragged(Config(**V3), cached, new, 3)
+    for args in ((), (200, 5)):
+        r.run(*args)
+        check_device_error()
+        r.check(*args)
+
+
 @pytest.mark.parametrize("heads", [128, 2])
 def test_caches_past_32_bits(heads):
     """Pages more than 4 GiB into the pool (and more than 2^31 values)."""

@@ -8,8 +8,9 @@ import subprocess
 from pathlib import Path
 
 import pytest
+import torch
 
-from mla_latent_kv_39_b200 import abi, build
+from mla_latent_kv_39_b200 import Config, RaggedLayer, abi, build
 
 ROOT = Path(__file__).resolve().parents[1]
 
@@ -257,3 +258,13 @@ def test_slots_and_stored_projection_refuse_bad_arguments(lib):
     assert lib.mla_out_proj_stored(P(c), OK, 4, OK, OK, OK, OK, need - 1, None) == abi.MLA_ERR_WORKSPACE
     assert lib.mla_out_proj_stored(P(c), None, 4, OK, OK, OK, OK, need, None) == abi.MLA_ERR_INVALID_ARG
     assert lib.mla_out_proj_stored(P(c), None, 0, None, None, None, None, 0, None) == abi.MLA_OK
+
+
+def test_a_ragged_layer_refuses_what_no_call_takes():
+    from types import SimpleNamespace
+    cache = SimpleNamespace(block_table=torch.zeros(abi.MAX_CHUNK_BATCH + 1, 1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="at most 8192 requests"):
+        RaggedLayer(Config(**V3), {}, cache, 1)
+    for bad in (dict(window=-1), dict(window=4, n_sinks=-1), dict(max_workers=-1)):
+        with pytest.raises(ValueError, match="negative"):
+            RaggedLayer(Config(**V3), {}, cache, 1, **bad)
