@@ -975,7 +975,8 @@ mla_status mla_batch_tables(const mla_config* cfg, int32_t batch, const int32_t*
     return MLA_ERR_INVALID_ARG;
   if (batch > tables::kMaxBatch || (long long)max_blocks_per_seq * cfg->block_size > INT32_MAX - cfg->block_size)
     return MLA_ERR_UNSUPPORTED;
-  const tables::Args a{batch, cfg->block_size, n_free, num_blocks, max_blocks_per_seq, n_tok, cached_lens, new_lens,
+  const tables::Args a{batch, cfg->block_size, n_free, num_blocks, max_blocks_per_seq, n_tok,
+                       (uint32_t)std::min<uint64_t>((1ull << 32) / (uint64_t)cfg->block_size, UINT32_MAX), cached_lens, new_lens,
                        free_blocks, free_head, block_table, cu_q, seq_lens, seq_idx, pos,
                        reinterpret_cast<long long*>(slots), free_head_out};
   return tables::launch(a, static_cast<cudaStream_t>(stream));

@@ -400,6 +400,12 @@ def test_batch_tables_reports_bad_entries():
     assert (got["slots"][:10] == -1).all() and (got["slots"][10:] >= 0).all()
 
 
+@pytest.mark.parametrize("bs", [1, 3, 100, 4096])
+def test_tables_of_long_requests_at_odd_page_sizes(bs):
+    Tables([2 ** 20, 2 ** 20 - 1, 5, 0], [3, 1, 0, 101], 2, bs).check()
+    check_device_error()
+
+
 def test_tables_at_the_largest_batch():
     n = 16384
     cached = [(7 * b) % 130 for b in range(n)]
