@@ -37,13 +37,16 @@
 // tensor pipe at 68% over a whole call (its own time is 4,352).  8 sequences of
 // 64 new tokens over 1k to 4k rows (315 GFLOP) take 266 us, 1.18 PFLOP/s; 1,024
 // new tokens of a 16k request (4.53 TFLOP) 3.35 ms, 1.35 PFLOP/s, by then at the
-// clock that the power limit leaves.  Decode steps are bound by the reads of
-// their pages from memory behind some 15 us of launch, planning and output.
+// clock that the power limit leaves.  In decode steps, whose pages no two tokens
+// share, a tile takes 10,000 clocks (5.3 us; 3.3 TB/s over 64 pairs) with its pages
+// in HBM and 7,800 with them in L2, behind some 15 us of launch, planning and
+// output.
 //
-// Measured and left out: pages fetched into L2 ahead (56 -> 65 us on a decode
-// step of 64 requests); scores two tiles ahead, the output kept in registers or
-// set aside in TMEM across pieces (1 to 14% slower); four load warps, eight more
-// warps for the output (2 to 6% slower).
+// Measured and left out: pages fetched into L2 ahead (bulk and single prefetches
+// cost as much as the loads they go ahead of, 54 -> 61 us on a decode step of 64
+// requests; plain loads neither gain nor lose); scores two tiles ahead, the output
+// kept in registers or set aside in TMEM across pieces (1 to 14% slower); four load
+// warps, eight more warps for the output (2 to 6% slower).
 //
 // TMEM (512 columns): scores [0, 128) and [128, 256), output [256, 512).
 // A pair MMA of M = 128 leaves a CTA's 64 rows in 128 lanes x N / 2 columns:
