@@ -533,7 +533,7 @@ def _chunk_args(cfg: Config, q, cu_q, cache: Cache, seq_lens, o_lat, workspace, 
     _need(workspace, "workspace", torch.uint8)
     if cache.pool.dtype != cfg.cache_torch_dtype or cache.pool.shape[1:] != (cfg.block_size, cfg.d_c + cfg.d_r):
         raise ValueError("cache pool dtype/shape does not match the config")
-    _need_here(q_lat, cu_q, seq_lens, cache.pool, o_lat, lse, workspace)
+    _need_here(q_lat, q_rope, cu_q, seq_lens, cache.pool, cache.block_table, cache.row_scale, o_lat, lse, workspace)
     return n, batch, q_lat, q_rope
 
 
@@ -568,6 +568,7 @@ def mla_out_proj_stored(cfg: Config, o_lat, W_UV, W_O, y, workspace, stream=None
     _need(W_O, "W_O", dt, shape=(H * cfg.v_head, cfg.hidden))
     _need(y, "y", dt, shape=(n, cfg.hidden))
     _need(workspace, "workspace", torch.uint8)
+    _need_here(o_lat, W_UV, W_O, y, workspace)
     _check(lib().mla_out_proj_stored(ctypes.byref(cfg.c()), _ptr(o_lat), n, _ptr(W_UV), _ptr(W_O), _ptr(y),
                                      _ptr(workspace), workspace.numel(), _stream(stream)), "mla_out_proj_stored")
 
