@@ -153,7 +153,7 @@ inline Layout layout(int workers) {
   Layout L{};
   L.workers = workers;
   size_t o = 0;
-  L.off_shares = o; o = align_up(o + sizeof(int4) * (size_t)workers, 256);
+  L.off_shares = o; o = align_up(o + sizeof(Shares) * (size_t)workers, 256);
   L.off_lse = o;   o = align_up(o + sizeof(float) * 2 * (size_t)workers * kH, 256);
   L.off_o = o;     o = align_up(o + sizeof(float) * 2 * (size_t)workers * kH * kDc, 256);
   L.total = o;
@@ -169,7 +169,7 @@ struct Params {
   int workers;
   float inv_workers;
   int single;       // a token to a worker, whatever the costs (then no merge follows)
-  int4* shares;     // the workers' Shares
+  Shares* shares;   // what the workers hold of cut tokens
   float* part_lse;
   float* part_o;
   bf16* o_lat;
@@ -451,7 +451,7 @@ __device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Param
   };
   const auto give_up = [&] {  // nothing to merge
     set_abort(sm);
-    if (rank == 0 && one) p.shares[worker] = make_int4(-1, -1, worker, -1);
+    if (rank == 0 && one) p.shares[worker] = Shares{-1, -1, worker, -1};
   };
   const auto load_query = [&](int tok) {
     if (one) {
@@ -536,7 +536,7 @@ __device__ void plan_role(Smem<kSplit>& sm, const CUtensorMap* qmap, const Param
   }
   __syncwarp();
   const Shares e = shares_of(p.q, cut, from, to, worker);
-  if (rank == 0 && one) p.shares[worker] = make_int4(e.continues, e.begins, e.last, e.first);
+  if (rank == 0 && one) p.shares[worker] = e;
   if (e.continues < 0)  // nothing of this worker's in its first place
     for (int h = lane; h < kHalfH; h += 32) p.part_lse[2LL * worker * kH + kHalfH * rank + h] = -INFINITY;
   __syncwarp();
@@ -982,17 +982,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Joins the pieces of the tokens that several workers share:
 //   o_lat = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).
 // Grid (workers, 8); most calls' workers share few tokens or none, and a block
-// without work costs its launch, so there are few.  A token of few pieces is
-// joined by the blocks of the worker that begins it, four heads at a time, one to
-// each 64 threads.  Of a token of many pieces (a long request) the blocks of up
-// to 32 of its workers take half a head at a time, the pieces dealt to the eight
-// warps: 256 blocks that read 75 KB each of 74 pieces (28 us by 32 blocks of
-// whole heads, 13 us by 128 of one head).  A thread owns 8 latent columns; three
-// loads are in flight, under no condition.  An idle worker's place counts as a
-// piece without visible rows (lse -inf).  Sums run in a fixed order.
-constexpr int kMergeThreads = 256, kMergeY = 8, kMergeFew = 8, kMergeMost = 32;
+// without work costs its launch, so there are few.  join_of (chunk_plan.cuh) says
+// which block joins what: of a token of few pieces four heads at a time, one to each
+// 64 threads; of a token of many pieces (a long request) half a head at a time, the
+// pieces dealt to the eight warps, over the blocks of up to 32 workers: 256 blocks
+// that read 75 KB each of 74 pieces (28 us by 32 blocks of whole heads, 13 us by 128
+// of one head).  A thread owns 8 latent columns; three loads are in flight, under no
+// condition.  An idle worker's place counts as a piece without visible rows (lse
+// -inf).  Sums run in a fixed order.
+constexpr int kMergeThreads = 256;
 
-__global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const int4* __restrict__ shares,
+__global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const Shares* __restrict__ shares,
                                                                        const float* __restrict__ part_lse,
                                                                        const float* __restrict__ part_o,
                                                                        bf16* __restrict__ o_lat,
@@ -1002,28 +1002,15 @@ __global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const int
   __shared__ float wt[kMaxWorkers + 4 * kMergeFew];  // weights: one list of many, or four of few
   __shared__ float4 sum[kMergeThreads / 32][2][32];
   const int w = blockIdx.x;
-  int4 own = shares[w];
-  int w0 = w;
-  if (own.y < 0 || own.z - w0 < kMergeFew) {  // not the first worker of a token of many pieces: one of its next?
-    if (own.w >= 0 && w - own.w < kMergeMost) {
-      const int4 head = shares[own.w];
-      if (head.z - own.w >= kMergeFew) {
-        w0 = own.w;
-        own = head;
-      }
-    }
-  }
-  const int tok = own.y, n = own.z - w0 + 1;
+  const Join j = join_of(shares, w);
+  const int tok = j.token, w0 = j.first, n = j.n, items = j.items(kH), step_item = j.step();
   if (tok < 0) return;
-  const bool many = n > kMergeFew;
+  const bool many = j.many();
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  // items: half a head of many pieces, four heads of few
-  const int helpers = many ? min(n, kMergeMost) : 1;
-  const int items = many ? 2 * kH : kH / 4, step_item = kMergeY * helpers;
   float* list = many ? wt : wt + kMergeFew * (warp / 2);
   // piece i: the beginning with worker w0, the rest with the workers behind it
   const auto slot_of = [&](int i) { return 2 * (w0 + i) + (i == 0 ? 1 : 0); };
-  for (int it = blockIdx.y + kMergeY * (w - w0); it < items; it += step_item) {
+  for (int it = j.begin(w, blockIdx.y); it < items; it += step_item) {
     const int h = many ? it / 2 : 4 * it + warp / 2;
     const int d = many ? kDc / 2 * (it & 1) + 8 * lane : 8 * (threadIdx.x % 64);
     if (many ? warp == 0 : warp % 2 == 0) {

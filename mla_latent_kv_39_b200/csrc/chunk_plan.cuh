@@ -292,7 +292,7 @@ struct Walk {
 // range begins inside a token, the worker that begins that one (-1 otherwise).
 // Workers between the first and the last may be without work: they continue no
 // token.
-struct Shares {
+struct alignas(16) Shares {
   int continues, begins, last, first;
 };
 __host__ __device__ inline Shares shares_of(const Batch& q, const Cut& cut, const Found& from, const Found& to, int w) {
@@ -317,6 +317,36 @@ __host__ __device__ inline Shares shares_of(const Batch& q, const Cut& cut, cons
     while (cut.at(e.last) >= end) --e.last;
   }
   return e;
+}
+
+// What the merge's blocks of worker w join: the pieces of one token, which are with
+// the workers first .. first + n - 1.  A token of up to kMergeFew pieces is joined by
+// the blocks of the worker that begins it, in items of four heads; one of more by those
+// of its first `helpers` workers, in items of half a head.  Block y takes the items
+// begin(w, y), begin(w, y) + step(), ...
+//
+// A block has one token only, so the worker that ends a token is never among its
+// helpers: its range goes on behind the token and may begin the next one, which it
+// then joins.  The ranges of the workers between the first and the last lie inside
+// the token whole, so those begin none.
+constexpr int kMergeY = 8, kMergeFew = 8, kMergeMost = 32;
+struct Join {
+  int token, first, n, helpers;  // token -1: nothing
+  __host__ __device__ bool many() const { return n > kMergeFew; }
+  __host__ __device__ int items(int heads) const { return many() ? 2 * heads : heads / 4; }
+  __host__ __device__ int begin(int w, int y) const { return y + kMergeY * (w - first); }
+  __host__ __device__ int step() const { return kMergeY * helpers; }
+};
+__host__ __device__ inline Join join_of(const Shares* shares, int w) {
+  Shares own = shares[w];
+  int first = w;
+  if (own.begins < 0 && own.first >= 0) {  // inside a token, or at its end
+    first = own.first;
+    own = shares[first];
+  }
+  const int n = own.last - first + 1;
+  const int helpers = n <= kMergeFew ? 1 : n - 1 < kMergeMost ? n - 1 : kMergeMost;
+  return {w - first < helpers ? own.begins : -1, first, n, helpers};
 }
 
 }  // namespace chunk

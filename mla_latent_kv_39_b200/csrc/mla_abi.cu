@@ -498,7 +498,7 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
                         workers,
                         1.f / workers,
                         whole ? 1 : 0,
-                        reinterpret_cast<int4*>(base + L.off_shares),
+                        reinterpret_cast<chunk::Shares*>(base + L.off_shares),
                         reinterpret_cast<float*>(base + L.off_lse),
                         reinterpret_cast<float*>(base + L.off_o),
                         o_lat,
@@ -518,7 +518,7 @@ mla_status chunk_tc_impl(const mla_config* c, const bf16* q, const chunk::Batch&
                    : chunk_pair_launch<false, chunk::PoolMap>(k, m, p, s)));
   if (whole) return MLA_OK;
   return st(launch_chained(chunk::chunk_merge_kernel, dim3(workers, chunk::kMergeY),
-                           dim3(chunk::kMergeThreads), 0, s, (const int4*)p.shares, (const float*)p.part_lse,
+                           dim3(chunk::kMergeThreads), 0, s, (const chunk::Shares*)p.shares, (const float*)p.part_lse,
                            (const float*)p.part_o, o_lat, lse));
 }
 
