@@ -115,6 +115,11 @@ typedef struct {
  * packed-query entry points return MLA_ERR_UNSUPPORTED for it. */
 #define MLA_FLAG_FP8_CACHE 2
 
+/* For mla_batch_tables (no effect elsewhere): the caller's token rows are laid out
+ * by new_lens already, so a request that is refused must not move the rows of the
+ * requests behind it; see there. */
+#define MLA_FLAG_FIXED_ROWS 4
+
 /* Paged latent cache of one layer ([P2] "MLA ve diğer optimizasyonlarla ilişkisi").
  * pool:        [num_blocks, block_size, d_c + d_r] storage dtype (E4M3 codes,
  *              one byte each, with MLA_FLAG_FP8_CACHE); row = [c_KV | k_R].
@@ -424,7 +429,11 @@ mla_status mla_combine_out_proj(const mla_config* cfg, const void* decode_ws, si
  * (MLA_ERR_UNSUPPORTED); batch 0 only with n_tok 0, a call without effect.
  * Device errors (MLA_ERR_BOUNDS):
  *   - a negative length, or more rows than a table row holds: that request
- *     gets no tokens and seq_lens 0;
+ *     gets no tokens and seq_lens 0, and those behind it are served, their rows
+ *     moved up (for callers that lay out their tokens by cu_q afterwards).  With
+ *     MLA_FLAG_FIXED_ROWS it and all behind it get no tokens and no pages, as
+ *     those that do not fit; seq_lens stays cached_lens where a table row holds
+ *     that many rows, and is 0 otherwise;
  *   - requests that do not fit into the n_tok rows or the free list: the first
  *     of them and all behind it get no tokens and no pages in this step
  *     (seq_lens stays cached_lens, so the caller sees which);

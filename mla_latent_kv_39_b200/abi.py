@@ -30,6 +30,7 @@ MLA_F32 = 0
 MLA_BF16 = 1
 MLA_FLAG_SPLIT_QUERY = 1
 MLA_FLAG_FP8_CACHE = 2
+MLA_FLAG_FIXED_ROWS = 4
 MLA_APPEND_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 # Every symbol the header declares, with (restype, argtypes).
@@ -145,6 +146,7 @@ class Config:
     dtype: str = "bf16"
     split_query: bool = False
     fp8_cache: bool = False       # E4M3 cache rows with one fp32 scale each (bf16 weights)
+    fixed_rows: bool = False      # mla_batch_tables: a refused request ends the served ones
 
     @staticmethod
     def from_shape(shape, split_query: bool = False, fp8_cache: bool = False) -> "Config":
@@ -173,7 +175,8 @@ class Config:
                          self.q_lora, self.rope_theta, self.softmax_scale, self.block_size,
                          MLA_BF16 if self.dtype == "bf16" else MLA_F32,
                          (MLA_FLAG_SPLIT_QUERY if self.split_query else 0)
-                         | (MLA_FLAG_FP8_CACHE if self.fp8_cache else 0))
+                         | (MLA_FLAG_FP8_CACHE if self.fp8_cache else 0)
+                         | (MLA_FLAG_FIXED_ROWS if self.fixed_rows else 0))
 
 
 class Cache:
@@ -464,7 +467,8 @@ def mla_batch_tables(cfg: Config, cached_lens, new_lens, free_blocks, free_head,
 
     ``block_table`` is extended in place with pages from ``free_blocks``; the cursor ``free_head`` moves on in
     ``free_head_out`` (default: in place).  ``seq_lens`` may be ``cached_lens``.  The token arrays ``seq_idx``,
-    ``pos`` and ``slots`` are padded with -1, 0 and -1 behind the last token."""
+    ``pos`` and ``slots`` are padded with -1, 0 and -1 behind the last token.  A caller whose token rows are laid
+    out by ``new_lens`` already passes a configuration with ``fixed_rows``."""
     batch, n_tok = cached_lens.shape[0], pos.shape[0]
     i32 = torch.int32
     free_head_out = free_head if free_head_out is None else free_head_out

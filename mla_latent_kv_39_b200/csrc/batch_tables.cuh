@@ -13,7 +13,8 @@
 //
 // Requests whose tokens or pages do not fit any more (and all behind them) get
 // no tokens and no pages; both prefix sums only grow, so "fits" is a prefix of
-// the requests.
+// the requests.  With fixed_rows a request with bad entries counts as one that does
+// not fit, so that nothing behind it moves; without, it is passed over.
 //
 // What bounds it is latency: 8 bytes read a request, 16 bytes written a token.
 // One cluster of 8 CTAs, each of which makes both prefix sums for itself
@@ -36,6 +37,7 @@ constexpr int kCtas = 8;
 
 struct Args {
   int batch, bs, n_free, num_blocks, max_blocks, n_tok;
+  int fixed_rows;
   uint32_t inv;  // floor(2^32 / bs), at most 2^32 - 1
   const int32_t* cached;
   const int32_t* new_;
@@ -134,17 +136,24 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
 #pragma unroll 4
   for (int b = tid; b < a.batch; b += kThreads) {
     const int c = a.cached[b], w = a.new_[b];
-    const bool bad = c < 0 || w < 0 || (long long)c + w > (long long)a.max_blocks * a.bs;
-    len[b] = bad ? -1 : c;
+    const long long rows = (long long)a.max_blocks * a.bs;
+    const bool bad = c < 0 || w < 0 || (long long)c + w > rows;
+    len[b] = bad && !(a.fixed_rows && c >= 0 && c <= rows) ? -1 : c;
     cu[b + 1] = bad ? 0 : w;
-    first[b + 1] = bad ? 0 : pages_of(c + w, a) - pages_of(c, a);
+    first[b + 1] = bad ? (a.fixed_rows ? -1 : 0) : pages_of(c + w, a) - pages_of(c, a);  // -1: ends the served requests
   }
   const int per = (a.batch + kThreads - 1) / kThreads | 1;  // odd: the threads' runs begin in different banks
   if (per > 1) __syncthreads();
   const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
   long long n = 0, pages = 0;
+  int miss = a.batch;  // the first request of this thread's that is not served
   for (int b = b0; b < b1; ++b) {
-    if (len[b] < 0 && rank == 0) report(MLA_ERR_BOUNDS, 30, b, a.cached[b] < 0 ? a.cached[b] : a.new_[b]);
+    if ((len[b] < 0 || first[b + 1] < 0) && rank == 0)
+      report(MLA_ERR_BOUNDS, 30, b, a.cached[b] < 0 ? a.cached[b] : a.new_[b]);
+    if (first[b + 1] < 0) {
+      first[b + 1] = 0;
+      miss = min(miss, b);
+    }
     n += cu[b + 1];
     pages += first[b + 1];
   }
@@ -157,11 +166,10 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
   scan2(n, pages, tot);
   n -= own_n;
   pages -= own_p;
-  int miss = a.batch;  // the first request of this thread's that does not fit
   for (int b = b0; b < b1; ++b) {
     n += cu[b + 1];
     pages += first[b + 1];
-    if (n > a.n_tok || pages > avail) {
+    if (b >= miss || n > a.n_tok || pages > avail) {
       miss = b;
       break;
     }

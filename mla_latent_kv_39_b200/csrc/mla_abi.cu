@@ -32,7 +32,7 @@ mla_status check_cfg(const mla_config* c) {
       !(c->rope_theta > 0.0) || c->softmax_scale < 0.f)
     return MLA_ERR_INVALID_ARG;
   if (c->dtype != MLA_F32 && c->dtype != MLA_BF16) return MLA_ERR_INVALID_ARG;
-  if (c->flags & ~(MLA_FLAG_SPLIT_QUERY | MLA_FLAG_FP8_CACHE)) return MLA_ERR_INVALID_ARG;
+  if (c->flags & ~(MLA_FLAG_SPLIT_QUERY | MLA_FLAG_FP8_CACHE | MLA_FLAG_FIXED_ROWS)) return MLA_ERR_INVALID_ARG;
   if ((c->flags & MLA_FLAG_FP8_CACHE) && c->dtype != MLA_BF16) return MLA_ERR_INVALID_ARG;
   return MLA_OK;
 }
@@ -976,6 +976,7 @@ mla_status mla_batch_tables(const mla_config* cfg, int32_t batch, const int32_t*
   if (batch > tables::kMaxBatch || (long long)max_blocks_per_seq * cfg->block_size > INT32_MAX - cfg->block_size)
     return MLA_ERR_UNSUPPORTED;
   const tables::Args a{batch, cfg->block_size, n_free, num_blocks, max_blocks_per_seq, n_tok,
+                       (cfg->flags & MLA_FLAG_FIXED_ROWS) != 0,
                        (uint32_t)std::min<uint64_t>((1ull << 32) / (uint64_t)cfg->block_size, UINT32_MAX), cached_lens, new_lens,
                        free_blocks, free_head, block_table, cu_q, seq_lens, seq_idx, pos,
                        reinterpret_cast<long long*>(slots), free_head_out};

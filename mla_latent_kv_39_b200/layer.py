@@ -9,6 +9,7 @@ splits, and apply W_UV / W_O.  All buffers are allocated once, up front.
 
 from __future__ import annotations
 
+import dataclasses
 from typing import Dict, Optional
 
 import torch
@@ -31,7 +32,6 @@ class DecodeLayer:
         # decode and the projections see.
         self.dcfg, self.dcache, self.fp8_scratch = cfg, cache, None
         if cfg.fp8_cache and packed_query:
-            import dataclasses
             self.dcfg = dataclasses.replace(cfg, fp8_cache=False)
             mb = cache.block_table.shape[1]
             self.fp8_scratch = torch.empty(abi.mla_fp8_scratch_bytes(cfg, batch, mb), dtype=torch.uint8, device=dev)
@@ -274,6 +274,12 @@ class RaggedLayer:
     first rows) and projects the output.  ``cache.block_table`` is extended in
     place.  ``window`` = 0: all rows up to the token's own.
 
+    A request that cannot be served (its rows are more than its table holds, or
+    the free pages or the token rows are used up) and all behind it wait: their
+    ``seq_lens`` stays, nothing is stored for them, their rows of ``y`` mean
+    nothing, and the device error word says so.  The caller takes it out (a
+    ``new_lens`` of 0) and goes on.
+
     Pages that have left a window may be given to other requests, with any entry
     left in the table; not so with an FP8 cache, whose step expands all pages
     that the lengths cover."""
@@ -288,10 +294,10 @@ class RaggedLayer:
         self.window, self.n_sinks, self.max_workers = window, n_sinks, max_workers
         dev, H = cache.pool.device, cfg.n_heads
         batch, width = cache.block_table.shape
+        self.tcfg = dataclasses.replace(cfg, fixed_rows=True)    # x is laid out by new_lens
         # an FP8 cache is expanded into a bf16 scratch for the step, as in DecodeLayer
         self.dcfg, self.dcache, self.fp8_scratch = cfg, cache, None
         if cfg.fp8_cache:
-            import dataclasses
             self.dcfg = dataclasses.replace(cfg, fp8_cache=False)
             self.fp8_scratch = torch.empty(abi.mla_fp8_scratch_bytes(cfg, batch, width), dtype=torch.uint8, device=dev)
             self.dcache = abi.fp8_scratch_cache(self.dcfg, self.fp8_scratch, batch, width)
@@ -319,7 +325,7 @@ class RaggedLayer:
 
     def tables(self, cached_lens, new_lens, free_blocks, free_head, stream=None):
         """Tables, positions and slots of a step; ``self.seq_lens`` afterwards holds the next step's ``cached_lens``."""
-        abi.mla_batch_tables(self.cfg, cached_lens, new_lens, free_blocks, free_head, self.cache.pool.shape[0],
+        abi.mla_batch_tables(self.tcfg, cached_lens, new_lens, free_blocks, free_head, self.cache.pool.shape[0],
                              self.cache.block_table, self.cu_q, self.seq_lens, self.seq_idx, self.pos, self.slots,
                              stream=stream)
 
