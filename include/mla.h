@@ -437,6 +437,8 @@ mla_status mla_combine_out_proj(const mla_config* cfg, const void* decode_ws, si
  *   - requests that do not fit into the n_tok rows or the free list: the first
  *     of them and all behind it get no tokens and no pages in this step
  *     (seq_lens stays cached_lens, so the caller sees which);
+ *   - *free_head outside [0, n_free]: nothing is handed out (requests that need no
+ *     page are served up to the first that does), *free_head_out = *free_head;
  *   - a block id outside the pool: slot -1 for its tokens.
  *
  * mla_cache_append_slots - mla_cache_append with the tokens' slots given

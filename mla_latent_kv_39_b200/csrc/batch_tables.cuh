@@ -128,9 +128,9 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
   pdl_wait();
   pdl_trigger();
 
-  int head = *a.free_head;
-  const bool bad_head = head < 0 || head > a.n_free;
-  if (bad_head) head = a.n_free;  // nothing to hand out
+  const int cursor = *a.free_head;
+  const bool bad_head = cursor < 0 || cursor > a.n_free;
+  const int head = bad_head ? a.n_free : cursor;  // bad: nothing to hand out, and the cursor stays what it is
   const int avail = a.n_free - head;
   // every request's own counts, until the scan
 #pragma unroll 4
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
   if (tid == 0) {
     served = a.batch;
     cu[0] = first[0] = 0;
-    if (bad_head && rank == 0) report(MLA_ERR_BOUNDS, 33, *a.free_head, a.n_free);
+    if (bad_head && rank == 0) report(MLA_ERR_BOUNDS, 33, cursor, a.n_free);
   }
   const long long own_n = n, own_p = pages;
   scan2(n, pages, tot);
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
       a.cu_q[b] = cu[b];
       if (b < a.batch) a.seq_lens[b] = len[b] < 0 ? 0 : len[b] + (cu[b + 1] - cu[b]);
     }
-    if (tid == 0) *a.head_out = head + first[a.batch];
+    if (tid == 0) *a.head_out = bad_head ? cursor : head + first[a.batch];
   }
   // new table entries: one per page taken
   const int step = ctas * kThreads, me = rank * kThreads + tid;

@@ -100,3 +100,23 @@ def test_a_layer_serves_what_lies_ahead_of_an_over_long_request():
     s.cached.copy_(s.layer.seq_lens)
     s.check([1, 0, 5])                                       # the caller takes the second out; the third goes on
     assert np.array_equal(s.layer.seq_lens.cpu().numpy(), [62, 30, 25])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("cursor", [-1, 10 ** 6, -2 ** 31])
+def test_a_cursor_outside_the_list_stays(cursor, in_place):
+    """Only requests that need no page, ahead of the first that does, are served; the cursor is not replaced."""
+    t = Tables([10, 100, 64, 7], [3, 1, 1, 2])
+    t.head = cursor
+    got = t.run(in_place=in_place)
+    assert mla_get_device_error()[0] == abi.MLA_ERR_BOUNDS
+    assert got["head_out"].tolist() == [cursor]
+    assert got["cu_q"].tolist() == [0, 3, 4, 4, 4] and got["seq_lens"].tolist() == [13, 101, 64, 7]
+    assert torch.equal(got["table"], t.table)
+
+
+def test_a_cursor_at_the_end_of_the_list_is_fine():
+    t = Tables([10, 100], [3, 1], spare=0, free=0)
+    t.check()
+    assert t.head == len(t.free)
+    check_device_error()
