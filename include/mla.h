@@ -488,7 +488,9 @@ mla_status mla_cache_append_slots(const mla_config* cfg, const void* x, int32_t 
  *            not grow with the lengths and need not be initialised.  Calls that
  *            may overlap on the GPU need one each.
  * 128 heads, d_c 512, d_r 64, pages of 64 and a bf16 cache run on the tensor
- * cores; every other shape on CUDA cores (d_c + d_r <= 1024, any block_size).
+ * cores; every other shape on CUDA cores (d_c + d_r <= 1024, any block_size).  Of
+ * bf16 queries in other shapes mla_absorb_q_packed makes none: pack them from
+ * mla_absorb_q's.
  * For a large FP8 cache expand the pages first (mla_cache_dequant_fp8).
  * batch <= 8192 (MLA_ERR_UNSUPPORTED).  MLA_ERR_INVALID_ARG for window <= 0 or
  * n_sinks < 0, pointers off their type's alignment (16 bytes on the tensor-core

@@ -261,6 +261,20 @@ class DecodeLayer:
         return y_host
 
 
+def _refuse_without_a_step(cfg: abi.Config):
+    """Configurations of which a ragged step's kernels do not take every part: bf16 queries are packed for the
+    tensor-core attention's shape only, and the CUDA-core attention takes rows of up to 1024 values."""
+    if cfg.dtype == "bf16":
+        shape = (cfg.n_heads, cfg.d_c, cfg.d_r, cfg.block_size)
+        if shape != (128, 512, 64, 64):
+            raise ValueError("RaggedLayer: bf16 takes 128 heads, d_c 512, d_r 64 and pages of 64, got "
+                             f"{cfg.n_heads}, {cfg.d_c}, {cfg.d_r} and {cfg.block_size}")
+        if abi.mla_out_proj_workspace_size(cfg, 1) == 0:
+            raise ValueError("RaggedLayer: no tensor-core projections of this hidden, q_lora, qk_nope or v_head")
+    elif cfg.d_c + cfg.d_r > 1024:
+        raise ValueError(f"RaggedLayer: rows of up to 1024 values, got {cfg.d_c + cfg.d_r}")
+
+
 class RaggedLayer:
     """One MLA layer's step for a batch whose requests bring different numbers
     of new tokens: none, one (a decode) or a prompt's chunk.
@@ -272,7 +286,9 @@ class RaggedLayer:
     from ``free_blocks``), projects the queries, stores the new latent rows
     through their slots, attends (causally, or over a sliding window and a few
     first rows) and projects the output.  ``cache.block_table`` is extended in
-    place.  ``window`` = 0: all rows up to the token's own.
+    place.  ``window`` = 0: all rows up to the token's own.  bf16 (with a bf16 or
+    FP8 cache) in the tensor-core shape: 128 heads, d_c 512, d_r 64, pages of 64;
+    fp32 in any shape of up to 1024 values a row.
 
     A request that cannot be served (its rows are more than its table holds, or
     the free pages or the token rows are used up) and all behind it wait: their
@@ -290,6 +306,7 @@ class RaggedLayer:
             raise ValueError("window, n_sinks and max_workers must not be negative")
         if cache.block_table.shape[0] > abi.MAX_CHUNK_BATCH:
             raise ValueError(f"at most {abi.MAX_CHUNK_BATCH} requests a step, got {cache.block_table.shape[0]}")
+        _refuse_without_a_step(cfg)
         self.cfg, self.W, self.cache, self.n_tok = cfg, weights, cache, n_tok
         self.window, self.n_sinks, self.max_workers = window, n_sinks, max_workers
         dev, H = cache.pool.device, cfg.n_heads
