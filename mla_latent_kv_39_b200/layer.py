@@ -359,26 +359,31 @@ class RaggedLayer:
     def step(self, x, cached_lens, new_lens, free_blocks, free_head, stream=None) -> torch.Tensor:
         """One step on device tensors: ``y`` ``[n_tok, hidden]`` (a reused buffer; padding rows mean nothing).
         ``free_head`` moves on in place; pass ``self.seq_lens`` as the next step's ``cached_lens``."""
+        W, cfg = self.W, self.dcfg
+        W_DQ, W_UQ, W_UK = W.get("W_DQ"), W["W_UQ"] if "W_UQ" in W else W["W_Q"], W["W_UK"]
+        W_DKV, W_KR, W_UV, W_O = W["W_DKV"], W["W_KR"], W["W_UV"], W["W_O"]
+        # the tables change the caller's state: what the later calls would refuse is refused ahead of them
+        abi._need(x, "x", cfg.torch_dtype, shape=(self.n_tok, cfg.hidden))
+        abi._need_here(x, self.cache.pool)
+        if cfg.dtype == "bf16" and x.data_ptr() % 16:
+            raise ValueError("x must start on a 16-byte boundary")
         main = stream or torch.cuda.current_stream()
         self.tables(cached_lens, new_lens, free_blocks, free_head, main)
         ready = torch.cuda.Event()
         ready.record(main)
-        W, cfg = self.W, self.dcfg
-        W_UQ = W["W_UQ"] if "W_UQ" in W else W["W_Q"]
         if cfg.dtype == "bf16":
-            abi.mla_absorb_q_packed(cfg, x, W.get("W_DQ"), W_UQ, W["W_UK"], self.pos, self.q, self.ws_gemm, main)
+            abi.mla_absorb_q_packed(cfg, x, W_DQ, W_UQ, W_UK, self.pos, self.q, self.ws_gemm, main)
         else:
-            abi.mla_absorb_q(cfg, x, W.get("W_DQ"), W_UQ, W["W_UK"], self.pos, *self.q, self.ws_gemm, main)
+            abi.mla_absorb_q(cfg, x, W_DQ, W_UQ, W_UK, self.pos, *self.q, self.ws_gemm, main)
         # the new rows on a second stream beside the query projections
         self.side.wait_event(ready)
-        abi.mla_cache_append_slots(self.cfg, x, W["W_DKV"], W["W_KR"], self.pos, self.slots, self.cache, self.ws_append,
-                                   self.side)
+        abi.mla_cache_append_slots(self.cfg, x, W_DKV, W_KR, self.pos, self.slots, self.cache, self.ws_append, self.side)
         done = torch.cuda.Event()
         done.record(self.side)
         main.wait_event(done)
         x.record_stream(self.side)
         self.attend(main)
-        abi.mla_out_proj_stored(cfg, self.o_lat, W["W_UV"], W["W_O"], self.y, self.ws_gemm, main)
+        abi.mla_out_proj_stored(cfg, self.o_lat, W_UV, W_O, self.y, self.ws_gemm, main)
         return self.y
 
     def capture_step(self, x, cached_lens, new_lens, free_blocks, free_head) -> torch.cuda.CUDAGraph:
