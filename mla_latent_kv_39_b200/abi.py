@@ -504,7 +504,7 @@ def mla_cache_append_slots(cfg: Config, x, W_DKV, W_KR, pos, slots, cache: Cache
     _need(workspace, "workspace", torch.uint8)
     if cache.pool.dtype != cfg.cache_torch_dtype or cache.pool.shape[1:] != (cfg.block_size, cfg.d_c + cfg.d_r):
         raise ValueError("cache pool dtype/shape does not match the config")
-    _need_here(x, W_DKV, W_KR, pos, slots, cache.pool, workspace)
+    _need_here(x, W_DKV, W_KR, pos, slots, cache.pool, cache.block_table, cache.row_scale, workspace)
     _check(lib().mla_cache_append_slots(ctypes.byref(cfg.c()), _ptr(x), n, _ptr(W_DKV), _ptr(W_KR), _ptr(pos),
                                         _ptr(slots), ctypes.byref(cache.c), _ptr(workspace), workspace.numel(),
                                         _stream(stream)), "mla_cache_append_slots")

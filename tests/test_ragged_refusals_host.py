@@ -25,3 +25,42 @@ def test_a_ragged_layer_refuses_shapes_that_no_step_computes(kw):
     cache = SimpleNamespace(block_table=torch.zeros(2, 3, dtype=torch.int32), pool=torch.zeros(1))
     with pytest.raises(ValueError, match="RaggedLayer"):
         RaggedLayer(Config(**{**V3, **kw}), {}, cache, 4)
+
+
+class Held(SimpleNamespace):
+    """What the checks ask of a tensor, on a device of its own."""
+
+    def __init__(self, shape, dtype=torch.int32, device=0):
+        super().__init__(shape=torch.Size(shape), dtype=dtype, device=f"cuda:{device}", index=device)
+
+    def get_device(self):
+        return self.index
+
+    def numel(self):
+        return self.shape.numel()
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+@pytest.fixture
+def first_device(monkeypatch):
+    def launched():
+        raise AssertionError("a call with a tensor of another device went through")
+    monkeypatch.setattr(abi, "_need", lambda *a, **k: None)
+    monkeypatch.setattr(abi, "lib", launched)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+
+def test_slots_are_stored_on_the_current_device_only(first_device):
+    cfg = Config(**V3, fp8_cache=True)
+    names = ["x", "W_DKV", "W_KR", "pos", "slots", "pool", "table", "row_scale", "workspace"]
+    for away in names + [None]:
+        at = {n: int(n == away) for n in names}
+        cache = SimpleNamespace(pool=Held((8, 64, 576), torch.uint8, at["pool"]), block_table=Held((2, 3), device=at["table"]),
+                                row_scale=Held((8, 64), torch.float32, at["row_scale"]), c=abi.MLACache())
+        args = (Held((4, 7168), torch.bfloat16, at["x"]), Held((7168, 512), torch.bfloat16, at["W_DKV"]),
+                Held((7168, 64), torch.bfloat16, at["W_KR"]), Held((4,), device=at["pos"]), Held((4,), torch.int64, at["slots"]),
+                cache, Held((1 << 20,), torch.uint8, at["workspace"]))
+        with pytest.raises(AssertionError if away is None else ValueError):
+            abi.mla_cache_append_slots(cfg, *args)
