@@ -461,6 +461,13 @@ def _need_here(*tensors):
             raise ValueError(f"every tensor must be on the current device cuda:{here}, got one on {t.device}")
 
 
+def _need_i32(**numbers):
+    """The library takes 32-bit numbers, and ctypes cuts others down to their low bits without a word."""
+    for name, v in numbers.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} must fit in 32 bits, got {v}")
+
+
 def mla_batch_tables(cfg: Config, cached_lens, new_lens, free_blocks, free_head, num_blocks: int, block_table, cu_q,
                      seq_lens, seq_idx, pos, slots, free_head_out=None, stream=None):
     """Block tables, prefix, positions and slots of a ragged step (``include/mla.h``).
@@ -485,6 +492,7 @@ def mla_batch_tables(cfg: Config, cached_lens, new_lens, free_blocks, free_head,
     _need(seq_idx, "seq_idx", i32, shape=(n_tok,))
     _need(pos, "pos", i32, shape=(n_tok,))
     _need(slots, "slots", torch.int64, shape=(n_tok,))
+    _need_i32(num_blocks=num_blocks)
     _need_here(cached_lens, new_lens, free_blocks, free_head, block_table, cu_q, seq_lens, seq_idx, pos, slots, free_head_out)
     _check(lib().mla_batch_tables(ctypes.byref(cfg.c()), batch, _ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks),
                                   free_blocks.shape[0], _ptr(free_head), num_blocks, _ptr(block_table),
@@ -511,6 +519,7 @@ def mla_cache_append_slots(cfg: Config, x, W_DKV, W_KR, pos, slots, cache: Cache
 
 
 def mla_chunk_workspace_size(cfg: Config, n_tok: int, max_workers: int = 0) -> int:
+    _need_i32(n_tok=n_tok, max_workers=max_workers)
     return int(lib().mla_chunk_workspace_size(ctypes.byref(cfg.c()), n_tok, max_workers))
 
 
@@ -546,6 +555,7 @@ def mla_chunk_attention(cfg: Config, q, cu_q, cache: Cache, seq_lens, o_lat, wor
     """Ragged causal attention of new tokens over the paged cache (``include/mla.h``).  ``q``: the packed bf16 rows,
     or for fp32 storage and an FP8 cache the pair ``(q_lat, q_rope)``.  Rows of ``o_lat`` and ``lse`` from
     ``cu_q[-1]`` on keep what they hold."""
+    _need_i32(max_workers=max_workers)
     n, batch, q_lat, q_rope = _chunk_args(cfg, q, cu_q, cache, seq_lens, o_lat, workspace, lse)
     _check(lib().mla_chunk_attention(ctypes.byref(cfg.c()), _ptr(q_lat), _ptr(q_rope), n, _ptr(cu_q), batch,
                                      ctypes.byref(cache.c), _ptr(seq_lens), max_workers, _ptr(o_lat), _ptr(lse),
@@ -555,6 +565,7 @@ def mla_chunk_attention(cfg: Config, q, cu_q, cache: Cache, seq_lens, o_lat, wor
 def mla_window_attention(cfg: Config, q, cu_q, cache: Cache, seq_lens, window: int, n_sinks: int, o_lat, workspace,
                          lse=None, max_workers: int = 0, stream=None):
     """``mla_chunk_attention`` over a sliding window of ``window`` rows and the first ``n_sinks`` rows."""
+    _need_i32(window=window, n_sinks=n_sinks, max_workers=max_workers)
     n, batch, q_lat, q_rope = _chunk_args(cfg, q, cu_q, cache, seq_lens, o_lat, workspace, lse)
     _check(lib().mla_window_attention(ctypes.byref(cfg.c()), _ptr(q_lat), _ptr(q_rope), n, _ptr(cu_q), batch,
                                       ctypes.byref(cache.c), _ptr(seq_lens), window, n_sinks, max_workers, _ptr(o_lat),

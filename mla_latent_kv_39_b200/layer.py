@@ -304,6 +304,7 @@ class RaggedLayer:
                  window: int = 0, n_sinks: int = 0, max_workers: int = 0):
         if window < 0 or n_sinks < 0 or max_workers < 0:
             raise ValueError("window, n_sinks and max_workers must not be negative")
+        abi._need_i32(window=window, n_sinks=n_sinks, max_workers=max_workers)
         if cache.block_table.shape[0] > abi.MAX_CHUNK_BATCH:
             raise ValueError(f"at most {abi.MAX_CHUNK_BATCH} requests a step, got {cache.block_table.shape[0]}")
         _refuse_without_a_step(cfg)

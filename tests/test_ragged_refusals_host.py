@@ -64,3 +64,42 @@ def test_slots_are_stored_on_the_current_device_only(first_device):
                 cache, Held((1 << 20,), torch.uint8, at["workspace"]))
         with pytest.raises(AssertionError if away is None else ValueError):
             abi.mla_cache_append_slots(cfg, *args)
+
+
+BIG = 2 ** 32 + 5          # its low 32 bits are 5: a number that would be taken
+
+
+def test_numbers_past_32_bits_are_refused_not_cut(first_device):
+    cfg = Config(**{**V3, "dtype": "f32"})
+    n = 4
+    cache = SimpleNamespace(pool=Held((8, 64, 576), torch.float32), block_table=Held((2, 3)), row_scale=None, c=abi.MLACache())
+    q, cu, lens = Held((n, 128, 576), torch.float32), Held((3,)), Held((2,))
+    o, ws = Held((n, 128, 512), torch.float32), Held((1 << 20,), torch.uint8)
+
+    def window(window=64, n_sinks=4, max_workers=0):
+        abi.mla_window_attention(cfg, (q, q), cu, cache, lens, window, n_sinks, o, ws, None, max_workers)
+
+    def chunk(max_workers=0):
+        abi.mla_chunk_attention(cfg, (q, q), cu, cache, lens, o, ws, None, max_workers)
+
+    def tables(num_blocks=8):
+        abi.mla_batch_tables(cfg, lens, lens, Held((5,)), Held((1,)), num_blocks, cache.block_table, cu, lens, Held((n,)),
+                             Held((n,)), Held((n,), torch.int64))
+    for call, names in ((window, ("window", "n_sinks", "max_workers")), (chunk, ("max_workers",)), (tables, ("num_blocks",))):
+        with pytest.raises(AssertionError):          # goes through as it is
+            call()
+        for name in names:
+            for bad in (BIG, 2 ** 31, -2 ** 31 - 1):
+                with pytest.raises(ValueError, match=name):
+                    call(**{name: bad})
+    with pytest.raises(ValueError, match="n_tok"):
+        abi.mla_chunk_workspace_size(cfg, BIG)
+    with pytest.raises(ValueError, match="max_workers"):
+        abi.mla_chunk_workspace_size(cfg, 4, BIG)
+
+
+def test_a_ragged_layer_refuses_numbers_past_32_bits():
+    cache = SimpleNamespace(block_table=torch.zeros(2, 3, dtype=torch.int32), pool=torch.zeros(1))
+    for name in ("window", "n_sinks", "max_workers"):
+        with pytest.raises(ValueError, match=name):
+            RaggedLayer(Config(**V3), {}, cache, 4, **{"window": 64, name: BIG})
