@@ -163,14 +163,16 @@ class Config:
         """Element type of the cache pool (uint8 E4M3 codes for an FP8 cache)."""
         return torch.uint8 if self.fp8_cache else self.torch_dtype
 
-    def c(self) -> MLAConfig:
-        c = self.__dict__.get("_c")      # made once: every call passes it
+    def _ref(self):
+        """What a call passes: a reference to a struct that is made once and handed to nobody else."""
+        c = self.__dict__.get("_c")
         if c is None:
-            c = self._make_c()
+            c = self.c()
             object.__setattr__(self, "_c", c)
-        return c
+        return ctypes.byref(c)
 
-    def _make_c(self) -> MLAConfig:
+    def c(self) -> MLAConfig:
+        """The C struct, the caller's own."""
         return MLAConfig(self.hidden, self.n_heads, self.d_c, self.d_r, self.qk_nope, self.v_head,
                          self.q_lora, self.rope_theta, self.softmax_scale, self.block_size,
                          MLA_BF16 if self.dtype == "bf16" else MLA_F32,
@@ -225,19 +227,19 @@ def _stream(stream) -> Optional[int]:
 # --------------------------------------------------------------- sizes
 
 def mla_cache_append_workspace_size(cfg: Config, n_tok: int) -> int:
-    return lib().mla_cache_append_workspace_size(ctypes.byref(cfg.c()), n_tok)
+    return lib().mla_cache_append_workspace_size(cfg._ref(), n_tok)
 
 
 def mla_absorb_q_workspace_size(cfg: Config, n_tok: int) -> int:
-    return lib().mla_absorb_q_workspace_size(ctypes.byref(cfg.c()), n_tok)
+    return lib().mla_absorb_q_workspace_size(cfg._ref(), n_tok)
 
 
 def mla_decode_workspace_size(cfg: Config, batch: int, n_q: int, max_workers: int = 0) -> int:
-    return lib().mla_decode_workspace_size(ctypes.byref(cfg.c()), batch, n_q, max_workers)
+    return lib().mla_decode_workspace_size(cfg._ref(), batch, n_q, max_workers)
 
 
 def mla_out_proj_workspace_size(cfg: Config, n_tok: int) -> int:
-    return lib().mla_out_proj_workspace_size(ctypes.byref(cfg.c()), n_tok)
+    return lib().mla_out_proj_workspace_size(cfg._ref(), n_tok)
 
 
 # --------------------------------------------------------------- the five steps
@@ -253,7 +255,7 @@ def mla_cache_append(cfg: Config, x, W_DKV, W_KR, seq_idx, pos, cache: Cache, wo
     _need(workspace, "workspace", torch.uint8)
     if cache.pool.dtype != cfg.cache_torch_dtype or cache.pool.shape[1:] != (cfg.block_size, cfg.d_c + cfg.d_r):
         raise ValueError("cache pool dtype/shape does not match the config")
-    _check(lib().mla_cache_append(ctypes.byref(cfg.c()), _ptr(x), n, _ptr(W_DKV), _ptr(W_KR),
+    _check(lib().mla_cache_append(cfg._ref(), _ptr(x), n, _ptr(W_DKV), _ptr(W_KR),
                                   _ptr(seq_idx), _ptr(pos), ctypes.byref(cache.c), _ptr(workspace),
                                   workspace.numel(), _stream(stream)), "mla_cache_append")
 
@@ -271,7 +273,7 @@ def mla_cache_append_noalloc(cfg: Config, x, W_DKV, W_KR, seq_idx, pos, cache: C
     _need(pos, "pos", torch.int32, shape=(n,))
     if cache.pool.dtype != cfg.cache_torch_dtype or cache.pool.shape[1:] != (cfg.block_size, cfg.d_c + cfg.d_r):
         raise ValueError("cache pool dtype/shape does not match the config")
-    _check(lib().mla_cache_append_noalloc(ctypes.byref(cfg.c()), _ptr(x), n, _ptr(W_DKV), _ptr(W_KR),
+    _check(lib().mla_cache_append_noalloc(cfg._ref(), _ptr(x), n, _ptr(W_DKV), _ptr(W_KR),
                                           _ptr(seq_idx), _ptr(pos), ctypes.byref(cache.c),
                                           _stream(stream)), "mla_cache_append_noalloc")
 
@@ -293,13 +295,13 @@ def mla_absorb_q(cfg: Config, x, W_DQ, W_UQ, W_UK, pos, q_lat, q_rope, workspace
     _need(q_lat, "q_lat", torch.float32, shape=(n, H, cfg.d_c))
     _need(q_rope, "q_rope", torch.float32, shape=(n, H, cfg.d_r))
     _need(workspace, "workspace", torch.uint8)
-    _check(lib().mla_absorb_q(ctypes.byref(cfg.c()), _ptr(x), n, _ptr(W_DQ), _ptr(W_UQ), _ptr(W_UK),
+    _check(lib().mla_absorb_q(cfg._ref(), _ptr(x), n, _ptr(W_DQ), _ptr(W_UQ), _ptr(W_UK),
                               _ptr(pos), _ptr(q_lat), _ptr(q_rope), _ptr(workspace), workspace.numel(),
                               _stream(stream)), "mla_absorb_q")
 
 
 def mla_query_packed_bytes(cfg: Config, n_tok: int) -> int:
-    return int(lib().mla_query_packed_bytes(ctypes.byref(cfg.c()), n_tok))
+    return int(lib().mla_query_packed_bytes(cfg._ref(), n_tok))
 
 
 def mla_absorb_q_packed(cfg: Config, x, W_DQ, W_UQ, W_UK, pos, q_packed, workspace, stream=None):
@@ -319,7 +321,7 @@ def mla_absorb_q_packed(cfg: Config, x, W_DQ, W_UQ, W_UK, pos, q_packed, workspa
     _need(q_packed, "q_packed", torch.bfloat16,
           shape=((2 if cfg.split_query else 1) * n, H, cfg.d_c + cfg.d_r))
     _need(workspace, "workspace", torch.uint8)
-    _check(lib().mla_absorb_q_packed(ctypes.byref(cfg.c()), _ptr(x), n, _ptr(W_DQ), _ptr(W_UQ), _ptr(W_UK),
+    _check(lib().mla_absorb_q_packed(cfg._ref(), _ptr(x), n, _ptr(W_DQ), _ptr(W_UQ), _ptr(W_UK),
                                      _ptr(pos), _ptr(q_packed), _ptr(workspace), workspace.numel(),
                                      _stream(stream)), "mla_absorb_q_packed")
 
@@ -331,7 +333,7 @@ def mla_decode_packed(cfg: Config, q_packed, batch: int, n_q: int, cache: Cache,
           shape=((2 if cfg.split_query else 1) * batch * n_q, H, cfg.d_c + cfg.d_r))
     _need(seq_lens, "seq_lens", torch.int32, shape=(batch,))
     _need(workspace, "workspace", torch.uint8)
-    _check(lib().mla_decode_packed(ctypes.byref(cfg.c()), _ptr(q_packed), batch, n_q, ctypes.byref(cache.c),
+    _check(lib().mla_decode_packed(cfg._ref(), _ptr(q_packed), batch, n_q, ctypes.byref(cache.c),
                                    _ptr(seq_lens), max_workers, _ptr(workspace), workspace.numel(),
                                    _stream(stream)), "mla_decode_packed")
 
@@ -340,7 +342,7 @@ def mla_decode_plan(cfg: Config, batch: int, n_q: int, cache: Cache, seq_lens, w
                     stream=None):
     _need(seq_lens, "seq_lens", torch.int32, shape=(batch,))
     _need(workspace, "workspace", torch.uint8)
-    _check(lib().mla_decode_plan(ctypes.byref(cfg.c()), batch, n_q, ctypes.byref(cache.c), _ptr(seq_lens),
+    _check(lib().mla_decode_plan(cfg._ref(), batch, n_q, ctypes.byref(cache.c), _ptr(seq_lens),
                                  max_workers, _ptr(workspace), workspace.numel(), _stream(stream)),
            "mla_decode_plan")
 
@@ -352,7 +354,7 @@ def mla_decode_packed_planned(cfg: Config, q_packed, batch: int, n_q: int, cache
           shape=((2 if cfg.split_query else 1) * batch * n_q, H, cfg.d_c + cfg.d_r))
     _need(seq_lens, "seq_lens", torch.int32, shape=(batch,))
     _need(workspace, "workspace", torch.uint8)
-    _check(lib().mla_decode_packed_planned(ctypes.byref(cfg.c()), _ptr(q_packed), batch, n_q,
+    _check(lib().mla_decode_packed_planned(cfg._ref(), _ptr(q_packed), batch, n_q,
                                            ctypes.byref(cache.c), _ptr(seq_lens), max_workers, _ptr(workspace),
                                            workspace.numel(), _stream(stream)), "mla_decode_packed_planned")
 
@@ -365,7 +367,7 @@ def mla_decode(cfg: Config, q_lat, q_rope, batch: int, n_q: int, cache: Cache, s
     _need(q_rope, "q_rope", torch.float32, shape=(batch * n_q, H, cfg.d_r))
     _need(seq_lens, "seq_lens", torch.int32, shape=(batch,))
     _need(workspace, "workspace", torch.uint8)
-    _check(lib().mla_decode(ctypes.byref(cfg.c()), _ptr(q_lat), _ptr(q_rope), batch, n_q,
+    _check(lib().mla_decode(cfg._ref(), _ptr(q_lat), _ptr(q_rope), batch, n_q,
                             ctypes.byref(cache.c), _ptr(seq_lens), max_workers, _ptr(workspace),
                             workspace.numel(), _stream(stream)), "mla_decode")
 
@@ -373,12 +375,12 @@ def mla_decode(cfg: Config, q_lat, q_rope, batch: int, n_q: int, cache: Cache, s
 def mla_combine(cfg: Config, workspace, batch: int, n_q: int, o_lat, stream=None):
     _need(workspace, "workspace", torch.uint8)
     _need(o_lat, "o_lat", torch.float32, shape=(batch * n_q, cfg.n_heads, cfg.d_c))
-    _check(lib().mla_combine(ctypes.byref(cfg.c()), _ptr(workspace), workspace.numel(), batch, n_q,
+    _check(lib().mla_combine(cfg._ref(), _ptr(workspace), workspace.numel(), batch, n_q,
                              _ptr(o_lat), _stream(stream)), "mla_combine")
 
 
 def mla_fp8_scratch_bytes(cfg: Config, batch: int, max_blocks_per_seq: int) -> int:
-    return int(lib().mla_fp8_scratch_bytes(ctypes.byref(cfg.c()), batch, max_blocks_per_seq))
+    return int(lib().mla_fp8_scratch_bytes(cfg._ref(), batch, max_blocks_per_seq))
 
 
 def fp8_scratch_cache(cfg: Config, scratch, batch: int, max_blocks_per_seq: int) -> "Cache":
@@ -395,7 +397,7 @@ def fp8_scratch_cache(cfg: Config, scratch, batch: int, max_blocks_per_seq: int)
 def mla_cache_dequant_fp8(cfg: Config, cache: "Cache", batch: int, seq_lens, scratch, stream=None):
     _need(seq_lens, "seq_lens", torch.int32, shape=(batch,))
     _need(scratch, "scratch", torch.uint8)
-    _check(lib().mla_cache_dequant_fp8(ctypes.byref(cfg.c()), ctypes.byref(cache.c), batch, _ptr(seq_lens),
+    _check(lib().mla_cache_dequant_fp8(cfg._ref(), ctypes.byref(cache.c), batch, _ptr(seq_lens),
                                        _ptr(scratch), scratch.numel(), _stream(stream)), "mla_cache_dequant_fp8")
 
 
@@ -403,7 +405,7 @@ def mla_combine_lse(cfg: Config, workspace, batch: int, n_q: int, o_lat, lse, st
     _need(workspace, "workspace", torch.uint8)
     _need(o_lat, "o_lat", torch.float32, shape=(batch * n_q, cfg.n_heads, cfg.d_c))
     _need(lse, "lse", torch.float32, shape=(batch * n_q, cfg.n_heads))
-    _check(lib().mla_combine_lse(ctypes.byref(cfg.c()), _ptr(workspace), workspace.numel(), batch, n_q,
+    _check(lib().mla_combine_lse(cfg._ref(), _ptr(workspace), workspace.numel(), batch, n_q,
                                  _ptr(o_lat), _ptr(lse), _stream(stream)), "mla_combine_lse")
 
 
@@ -415,12 +417,12 @@ def mla_merge_shards(cfg: Config, o_parts, lse_parts, o_lat, lse=None, stream=No
     _need(o_lat, "o_lat", torch.float32, shape=(rows, cfg.n_heads, cfg.d_c))
     if lse is not None:
         _need(lse, "lse", torch.float32, shape=(rows, cfg.n_heads))
-    _check(lib().mla_merge_shards(ctypes.byref(cfg.c()), S, rows, _ptr(o_parts), _ptr(lse_parts), _ptr(o_lat),
+    _check(lib().mla_merge_shards(cfg._ref(), S, rows, _ptr(o_parts), _ptr(lse_parts), _ptr(o_lat),
                                   _ptr(lse), _stream(stream)), "mla_merge_shards")
 
 
 def mla_combine_out_proj_workspace_size(cfg: Config, batch: int, n_q: int) -> int:
-    return int(lib().mla_combine_out_proj_workspace_size(ctypes.byref(cfg.c()), batch, n_q))
+    return int(lib().mla_combine_out_proj_workspace_size(cfg._ref(), batch, n_q))
 
 
 def mla_combine_out_proj(cfg: Config, decode_ws, batch: int, n_q: int, W_UV, W_O, y, workspace,
@@ -432,7 +434,7 @@ def mla_combine_out_proj(cfg: Config, decode_ws, batch: int, n_q: int, W_UV, W_O
     _need(W_O, "W_O", dt, shape=(H * cfg.v_head, cfg.hidden))
     _need(y, "y", dt, shape=(batch * n_q, cfg.hidden))
     _need(workspace, "workspace", torch.uint8)
-    _check(lib().mla_combine_out_proj(ctypes.byref(cfg.c()), _ptr(decode_ws), decode_ws.numel(), batch, n_q,
+    _check(lib().mla_combine_out_proj(cfg._ref(), _ptr(decode_ws), decode_ws.numel(), batch, n_q,
                                       max_workers, _ptr(W_UV), _ptr(W_O), _ptr(y), _ptr(workspace),
                                       workspace.numel(), _stream(stream)), "mla_combine_out_proj")
 
@@ -446,7 +448,7 @@ def mla_out_proj(cfg: Config, o_lat, W_UV, W_O, y, workspace, stream=None):
     _need(W_O, "W_O", dt, shape=(H * cfg.v_head, cfg.hidden))
     _need(y, "y", dt, shape=(n, cfg.hidden))
     _need(workspace, "workspace", torch.uint8)
-    _check(lib().mla_out_proj(ctypes.byref(cfg.c()), _ptr(o_lat), n, _ptr(W_UV), _ptr(W_O), _ptr(y),
+    _check(lib().mla_out_proj(cfg._ref(), _ptr(o_lat), n, _ptr(W_UV), _ptr(W_O), _ptr(y),
                               _ptr(workspace), workspace.numel(), _stream(stream)), "mla_out_proj")
 
 
@@ -494,7 +496,7 @@ def mla_batch_tables(cfg: Config, cached_lens, new_lens, free_blocks, free_head,
     _need(slots, "slots", torch.int64, shape=(n_tok,))
     _need_i32(num_blocks=num_blocks)
     _need_here(cached_lens, new_lens, free_blocks, free_head, block_table, cu_q, seq_lens, seq_idx, pos, slots, free_head_out)
-    _check(lib().mla_batch_tables(ctypes.byref(cfg.c()), batch, _ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks),
+    _check(lib().mla_batch_tables(cfg._ref(), batch, _ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks),
                                   free_blocks.shape[0], _ptr(free_head), num_blocks, _ptr(block_table),
                                   block_table.shape[1], n_tok, _ptr(cu_q), _ptr(seq_lens), _ptr(seq_idx), _ptr(pos),
                                   _ptr(slots), _ptr(free_head_out), _stream(stream)), "mla_batch_tables")
@@ -513,14 +515,14 @@ def mla_cache_append_slots(cfg: Config, x, W_DKV, W_KR, pos, slots, cache: Cache
     if cache.pool.dtype != cfg.cache_torch_dtype or cache.pool.shape[1:] != (cfg.block_size, cfg.d_c + cfg.d_r):
         raise ValueError("cache pool dtype/shape does not match the config")
     _need_here(x, W_DKV, W_KR, pos, slots, cache.pool, cache.block_table, cache.row_scale, workspace)
-    _check(lib().mla_cache_append_slots(ctypes.byref(cfg.c()), _ptr(x), n, _ptr(W_DKV), _ptr(W_KR), _ptr(pos),
+    _check(lib().mla_cache_append_slots(cfg._ref(), _ptr(x), n, _ptr(W_DKV), _ptr(W_KR), _ptr(pos),
                                         _ptr(slots), ctypes.byref(cache.c), _ptr(workspace), workspace.numel(),
                                         _stream(stream)), "mla_cache_append_slots")
 
 
 def mla_chunk_workspace_size(cfg: Config, n_tok: int, max_workers: int = 0) -> int:
     _need_i32(n_tok=n_tok, max_workers=max_workers)
-    return int(lib().mla_chunk_workspace_size(ctypes.byref(cfg.c()), n_tok, max_workers))
+    return int(lib().mla_chunk_workspace_size(cfg._ref(), n_tok, max_workers))
 
 
 def _chunk_args(cfg: Config, q, cu_q, cache: Cache, seq_lens, o_lat, workspace, lse):
@@ -557,7 +559,7 @@ def mla_chunk_attention(cfg: Config, q, cu_q, cache: Cache, seq_lens, o_lat, wor
     ``cu_q[-1]`` on keep what they hold."""
     _need_i32(max_workers=max_workers)
     n, batch, q_lat, q_rope = _chunk_args(cfg, q, cu_q, cache, seq_lens, o_lat, workspace, lse)
-    _check(lib().mla_chunk_attention(ctypes.byref(cfg.c()), _ptr(q_lat), _ptr(q_rope), n, _ptr(cu_q), batch,
+    _check(lib().mla_chunk_attention(cfg._ref(), _ptr(q_lat), _ptr(q_rope), n, _ptr(cu_q), batch,
                                      ctypes.byref(cache.c), _ptr(seq_lens), max_workers, _ptr(o_lat), _ptr(lse),
                                      _ptr(workspace), workspace.numel(), _stream(stream)), "mla_chunk_attention")
 
@@ -567,7 +569,7 @@ def mla_window_attention(cfg: Config, q, cu_q, cache: Cache, seq_lens, window: i
     """``mla_chunk_attention`` over a sliding window of ``window`` rows and the first ``n_sinks`` rows."""
     _need_i32(window=window, n_sinks=n_sinks, max_workers=max_workers)
     n, batch, q_lat, q_rope = _chunk_args(cfg, q, cu_q, cache, seq_lens, o_lat, workspace, lse)
-    _check(lib().mla_window_attention(ctypes.byref(cfg.c()), _ptr(q_lat), _ptr(q_rope), n, _ptr(cu_q), batch,
+    _check(lib().mla_window_attention(cfg._ref(), _ptr(q_lat), _ptr(q_rope), n, _ptr(cu_q), batch,
                                       ctypes.byref(cache.c), _ptr(seq_lens), window, n_sinks, max_workers, _ptr(o_lat),
                                       _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)),
            "mla_window_attention")
@@ -584,7 +586,7 @@ def mla_out_proj_stored(cfg: Config, o_lat, W_UV, W_O, y, workspace, stream=None
     _need(y, "y", dt, shape=(n, cfg.hidden))
     _need(workspace, "workspace", torch.uint8)
     _need_here(o_lat, W_UV, W_O, y, workspace)
-    _check(lib().mla_out_proj_stored(ctypes.byref(cfg.c()), _ptr(o_lat), n, _ptr(W_UV), _ptr(W_O), _ptr(y),
+    _check(lib().mla_out_proj_stored(cfg._ref(), _ptr(o_lat), n, _ptr(W_UV), _ptr(W_O), _ptr(y),
                                      _ptr(workspace), workspace.numel(), _stream(stream)), "mla_out_proj_stored")
 
 

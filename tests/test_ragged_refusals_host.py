@@ -103,3 +103,17 @@ def test_a_ragged_layer_refuses_numbers_past_32_bits():
     for name in ("window", "n_sinks", "max_workers"):
         with pytest.raises(ValueError, match=name):
             RaggedLayer(Config(**V3), {}, cache, 4, **{"window": 64, name: BIG})
+
+
+def test_a_config_keeps_its_numbers_when_a_caller_alters_the_struct():
+    """c() is the caller's own; what later calls pass is not altered through it, and equal configurations stay equal."""
+    cfg = Config(**V3)
+    c = cfg.c()
+    c.n_heads, c.flags = 7, 2
+    assert cfg.c().n_heads == 128 and cfg.c().flags == 0
+    assert abi.mla_chunk_workspace_size(cfg, 4) == abi.mla_chunk_workspace_size(Config(**V3), 4) > 256
+    assert cfg == Config(**V3) and hash(cfg) == hash(Config(**V3))
+    import copy
+    import pickle
+    for other in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg))):
+        assert other == cfg and abi.mla_chunk_workspace_size(other, 4) == abi.mla_chunk_workspace_size(cfg, 4)
