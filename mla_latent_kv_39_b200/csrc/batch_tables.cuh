@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
     const bool bad = c < 0 || w < 0 || (long long)c + w > rows;
     len[b] = bad && !(a.fixed_rows && c >= 0 && c <= rows) ? -1 : c;
     cu[b + 1] = bad ? 0 : w;
-    first[b + 1] = bad ? (a.fixed_rows ? -1 : 0) : pages_of(c + w, a) - pages_of(c, a);  // -1: ends the served requests
+    first[b + 1] = bad ? -1 : pages_of(c + w, a) - pages_of(c, a);
   }
   const int per = (a.batch + kThreads - 1) / kThreads | 1;  // odd: the threads' runs begin in different banks
   if (per > 1) __syncthreads();
@@ -148,14 +148,14 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const Args a) {
   long long n = 0, pages = 0;
   int miss = a.batch;  // the first request of this thread's that is not served
   for (int b = b0; b < b1; ++b) {
-    if ((len[b] < 0 || first[b + 1] < 0) && rank == 0)
-      report(MLA_ERR_BOUNDS, 30, b, a.cached[b] < 0 ? a.cached[b] : a.new_[b]);
-    if (first[b + 1] < 0) {
-      first[b + 1] = 0;
-      miss = min(miss, b);
+    int taken = first[b + 1];
+    if (taken < 0) {
+      if (rank == 0) report(MLA_ERR_BOUNDS, 30, b, a.cached[b] < 0 ? a.cached[b] : a.new_[b]);
+      if (a.fixed_rows) miss = min(miss, b);
+      first[b + 1] = taken = 0;
     }
     n += cu[b + 1];
-    pages += first[b + 1];
+    pages += taken;
   }
   if (tid == 0) {
     served = a.batch;
