@@ -19,9 +19,9 @@
 // What bounds it is latency: 8 bytes read a request, 16 bytes written a token.
 // One cluster of 8 CTAs, each of which makes both prefix sums for itself
 // (a scan of at most 16,384 values costs less than handing them round) and
-// then fills its share of the tokens: 3.5 us in a graph for 64 requests of a token
-// each (one CTA alone 3.6), 4.4 for 512 of 16 (13.2), 9.7 for 64 of 1024 (66), 16
-// for 16,384 of one (72).  Inputs that an output may replace (the
+// then fills its share of the tokens: 4 us for 64 requests of a token each (one CTA
+// alone the same), 4.8 for 512 of 16 (13.2), 10.3 for 64 of 1024 (66), 16 for 16,384
+// of one (72), one call behind the other in a graph.  Inputs that an output may replace (the
 // lengths by seq_lens, the cursor by its new value) are read by all CTAs before
 // the cluster's barrier and written behind it; one launch and no workspace.
 #pragma once

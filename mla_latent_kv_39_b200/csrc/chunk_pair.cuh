@@ -35,12 +35,13 @@
 // each SM's: 414 KB of operands into the MMAs, 278 KB from TMA, 32 KB of P.  At
 // 128 B per clock that is 5,656 clocks; measured are 5,620 a tile, with the
 // tensor pipe at 68% over a whole call (its own time is 4,352).  8 sequences of
-// 64 new tokens over 1k to 4k rows (315 GFLOP) take 266 us, 1.18 PFLOP/s; 1,024
-// new tokens of a 16k request (4.53 TFLOP) 3.35 ms, 1.35 PFLOP/s, by then at the
-// clock that the power limit leaves.  In decode steps, whose pages no two tokens
-// share, a tile takes 10,000 clocks (5.3 us; 3.3 TB/s over 64 pairs) with its pages
-// in HBM and 7,800 with them in L2, behind some 15 us of launch, planning and
-// output.
+// 64 new tokens over 1k to 4k rows (315 GFLOP) take 252 to 302 us, 1.25 to 1.04
+// PFLOP/s, on a cool GPU and behind minutes of load; 1,024 new tokens of a 16k
+// request (4.53 TFLOP) 3.33 to 3.70 ms, 1.36 to 1.22 PFLOP/s, at the clock that the
+// power limit leaves.  In decode steps, whose pages no two tokens share, a tile takes
+// 10,000 clocks (5.2 us; 3.6 TB/s over 64 pairs) with its pages in HBM and 7,800 with
+// them in L2, behind 7 us of planning and output where calls follow one another, some
+// 15 with the launch of a call alone.
 //
 // Measured and left out: pages fetched into L2 ahead (bulk and single prefetches
 // cost as much as the loads they go ahead of, 54 -> 61 us on a decode step of 64
@@ -823,6 +824,11 @@ struct Softmax {
         m_used = m_tile;
       }
       const float base = m_used == -INFINITY ? 0.f : -m_used * p.scale_log2;
+      // P goes into the MMA in bf16, as the values do (both operands of an MMA have one
+      // type, and one in fp32 would be read at half the rate): half a step of 2^-8 a weight, of either sign, which
+      // leaves o_lat 0.0021 (rms, relative) from the exact result where rounding that
+      // result alone leaves 0.0017.  The row sum takes the unrounded weights, so the
+      // log-sum-exp has none of it; sums and the pieces' outputs are fp32.
       uint32_t pk[32];
       if (hi > lo) {
         const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(base, base);

@@ -281,7 +281,7 @@ class RaggedLayer:
 
     All new tokens lie one behind the other in ``x`` ``[n_tok, hidden]``, request
     by request; rows behind the last token are padding (``n_tok`` is the largest
-    step's), so that one captured graph serves every step.  A step builds the
+    step's), so that one captured graph can serve every step.  A step builds the
     tables on the device (``mla_batch_tables``: pages for the new tokens come
     from ``free_blocks``), projects the queries, stores the new latent rows
     through their slots, attends (causally, or over a sliding window and a few
@@ -298,7 +298,12 @@ class RaggedLayer:
 
     Pages that have left a window may be given to other requests, with any entry
     left in the table; not so with an FP8 cache, whose step expands all pages
-    that the lengths cover."""
+    that the lengths cover, in time too (64 requests, window 2048: 145 us over
+    4,000 rows, 379 over 16,000).
+
+    The projections and the append take all ``n_tok`` rows, padding included: 64
+    decodes cost 0.27 ms in a step of 64 rows and 1.40 in one of 1,024, so a
+    server captures a graph for its decode steps beside that for prompts."""
 
     def __init__(self, cfg: abi.Config, weights: Dict[str, torch.Tensor], cache: abi.Cache, n_tok: int,
                  window: int = 0, n_sinks: int = 0, max_workers: int = 0):
